@@ -19,24 +19,24 @@ NIBBLES = (0, 2, 4, 6, 1, 3, 5, 7)  # k of nibble i inside a 32-bit word of the 
 def listed():
     return [
         # one sequence generating: the gate and up projections of one token stream both weight matrices
-        dict(name="gated, one token", op="gated", M=1, K=4096, N=14336, G=128, act="silu", save=False),
+        dict(name="gated one token", op="gated", M=1, K=4096, N=14336, G=128, act="silu", save=False),
         # a decode batch of 16 sequences, finer groups, the tanh GELU
-        dict(name="gated, decode batch", op="gated", M=16, K=4096, N=14336, G=64, act="gelu_tanh", save=False),
+        dict(name="gated decode batch", op="gated", M=16, K=4096, N=14336, G=64, act="gelu_tanh", save=False),
         # a short prompt through a small model of odd sizes (no multiple of a tile in any direction)
-        dict(name="gated, odd sizes", op="gated", M=333, K=1112, N=2856, G=48, act="gelu_erf", save=False),
+        dict(name="gated odd sizes", op="gated", M=333, K=1112, N=2856, G=48, act="gelu_erf", save=False),
         # a training batch: the forward pass keeps both projections for its backward pass
-        dict(name="gated, training forward", op="gated", M=2048, K=4096, N=14336, G=128, act="silu", save=True),
+        dict(name="gated training forward", op="gated", M=2048, K=4096, N=14336, G=128, act="silu", save=True),
         # the same batch backward, to the block's input
         dict(name="gated backward", op="gated_backward", M=2048, K=4096, N=14336, G=128, act="silu"),
-        dict(name="gated backward, odd sizes", op="gated_backward", M=77, K=1112, N=2856, G=48, act="gelu_erf"),
+        dict(name="gated backward odd sizes", op="gated_backward", M=77, K=1112, N=2856, G=48, act="gelu_erf"),
         # backward through an attention projection, and through the down projection of a short batch
-        dict(name="dgrad, projection", op="dgrad", M=2048, K=4096, N=4096, G=128),
-        dict(name="dgrad, down projection", op="dgrad", M=300, K=14336, N=4096, G=64),
+        dict(name="dgrad projection", op="dgrad", M=2048, K=4096, N=4096, G=128),
+        dict(name="dgrad down projection", op="dgrad", M=300, K=14336, N=4096, G=64),
         # one sequence with its adapter; 16 sequences with 16 adapters; five prompts side by side; many adapters, odd sizes
-        dict(name="lora, one token", op="lora", M=1, K=4096, N=4096, G=128, L=8, R=16, segs=0),
-        dict(name="lora, decode batch", op="lora", M=16, K=4096, N=14336, G=128, L=16, R=64, segs=0),
-        dict(name="lora, prompts", op="lora", M=2048, K=4096, N=4096, G=128, L=8, R=16, segs=5),
-        dict(name="lora, odd sizes", op="lora", M=200, K=1112, N=2856, G=48, L=40, R=24, segs=0),
+        dict(name="lora one token", op="lora", M=1, K=4096, N=4096, G=128, L=8, R=16, segs=0),
+        dict(name="lora decode batch", op="lora", M=16, K=4096, N=14336, G=128, L=16, R=64, segs=0),
+        dict(name="lora prompts", op="lora", M=2048, K=4096, N=4096, G=128, L=8, R=16, segs=5),
+        dict(name="lora odd sizes", op="lora", M=200, K=1112, N=2856, G=48, L=40, R=24, segs=0),
     ]
 
 
