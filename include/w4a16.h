@@ -82,7 +82,8 @@ enum {
     W4A16_ACT_IDENTITY = 0,
     W4A16_ACT_RELU = 1,
     W4A16_ACT_GELU_ERF = 2,
-    W4A16_ACT_GELU_TANH = 3
+    W4A16_ACT_GELU_TANH = 3,
+    W4A16_ACT_SILU = 4 /* x / (1 + e^-x): the gated entry points only */
 };
 
 /* Largest topK the expert layer accepts. */
@@ -287,6 +288,30 @@ int w4a16_moe_layer_static(const w4a16_half* X_dev, const w4a16_half* logits_dev
 
 /* Size in bytes of the static scratch region of w4a16_moe_layer_static. */
 int64_t w4a16_moe_static_scratch_bytes(void);
+
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward projections and the products a backward pass needs,
+ * on the same 4-bit weights (tiled layout). W stands for the fp16 matrix
+ * W[k, n] = fp16(q[k, n] * s[floor(k / G), n]); every product is accumulated in
+ * fp32. The codes and scales are constants here: nothing computes a gradient
+ * for them.
+ * ------------------------------------------------------------------------- */
+
+/* Gated projections: H_dev [M, N] = fp16(act(A W_gate) * (A W_up)) from
+ * activations A_dev [M, K] and two weight matrices [K -> N] of one group size
+ * G. Both products, the activation (any W4A16_ACT_*, SILU included) and their
+ * product are fp32; H is rounded once. If Pg_dev and Pu_dev are given (both or
+ * neither), the projections themselves are also written, Pg_dev = fp16(A W_gate)
+ * and Pu_dev = fp16(A W_up), both [M, N]: what w4a16_gated_gemm_backward reads.
+ * flags: 0 or W4A16_FLAG_STATIC_WEIGHTS (as for w4a16_gemm_ex; it covers both
+ * weight matrices). Contract of w4a16_gemm otherwise; H, Pg and Pu 2-byte
+ * aligned, and none of the outputs may overlap A or another output. M == 0 is a
+ * no-op. Errors: INVALID_ARG (also an unknown act or flag, or one of Pg and Pu
+ * alone), MISALIGNED, UNSUPPORTED, CUDA. */
+int w4a16_gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate_dev, const w4a16_half* S_gate_dev,
+                     const uint8_t* Wt_up_dev, const w4a16_half* S_up_dev, w4a16_half* H_dev, w4a16_half* Pg_dev,
+                     w4a16_half* Pu_dev, int64_t M, int64_t N, int64_t K, int64_t G, int act, uint32_t flags,
+                     void* stream);
 
 /* Declares (enable != 0) or withdraws (enable == 0) the promise that no
  * kernel on the calling streams writes the tiled weights or the scales passed

@@ -1,0 +1,31 @@
+"""Host-side refusals of the operators on frozen 4-bit weights: nothing is enqueued for a bad argument."""
+import pytest
+
+import weight_only_int4_wise_b200 as w
+from weight_only_int4_wise_b200 import build
+
+FAKE = 0x10000  # a non-null, 16-byte aligned address that is never dereferenced on these paths
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+
+
+def test_gated_gemm_rejects_bad_arguments_on_host():
+    def g(A=FAKE, wg=FAKE, sg=FAKE, wu=FAKE, su=FAKE, H=FAKE, Pg=None, Pu=None, M=4, N=128, K=128, G=64,
+          act=w.ACT_SILU, flags=0):
+        return w.w4a16_gated_gemm(A, wg, sg, wu, su, H, Pg, Pu, M, N, K, G, act, flags, stream=0)
+    for name in ("A", "wg", "sg", "wu", "su", "H"):
+        assert g(**{name: None}) == w.ERR_INVALID_ARG, name
+    assert g(Pg=FAKE) == w.ERR_INVALID_ARG and g(Pu=FAKE) == w.ERR_INVALID_ARG  # both or neither
+    assert g(M=-1) == w.ERR_INVALID_ARG and g(N=0) == w.ERR_INVALID_ARG
+    assert g(act=5) == w.ERR_INVALID_ARG and g(act=-1) == w.ERR_INVALID_ARG
+    assert g(flags=2) == w.ERR_INVALID_ARG
+    assert g(N=100) == w.ERR_UNSUPPORTED and g(K=100) == w.ERR_UNSUPPORTED and g(G=24) == w.ERR_UNSUPPORTED
+    assert g(M=1 << 31) == w.ERR_UNSUPPORTED
+    for name in ("A", "wg", "sg", "wu", "su"):
+        assert g(**{name: FAKE + 8}) == w.ERR_MISALIGNED, name
+    assert g(H=FAKE + 1) == w.ERR_MISALIGNED
+    assert g(Pg=FAKE + 1, Pu=FAKE) == w.ERR_MISALIGNED
+    assert g(M=0) == w.OK and g(M=0, Pg=FAKE, Pu=FAKE) == w.OK

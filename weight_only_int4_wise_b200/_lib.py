@@ -32,6 +32,7 @@ ACT_IDENTITY = 0
 ACT_RELU = 1
 ACT_GELU_ERF = 2
 ACT_GELU_TANH = 3
+ACT_SILU = 4  # the gated entry points only
 
 EXPORTED = [
     "w4a16_status_string", "w4a16_pack", "w4a16_unpack", "w4a16_tiled_bytes", "w4a16_repack",
@@ -42,6 +43,7 @@ EXPORTED = [
     "w4a16_set_tactic", "w4a16_get_tactic", "w4a16_clear_tactics", "w4a16_autotune",
     "w8a16_tiled_bytes", "w8a16_repack", "w8a16_gemm", "w8a16_gemm_launch_info",
     "w4a16_moe_layer_static", "w4a16_moe_static_scratch_bytes", "w4a16_gemm_ex", "w8a16_quantize",
+    "w4a16_gated_gemm",
 ]
 
 
@@ -148,6 +150,8 @@ def load() -> ctypes.CDLL:
                                        _i64, _i64, ctypes.c_int32, _i32p, ctypes.POINTER(ctypes.c_float),
                                        ctypes.POINTER(ctypes.c_float), ctypes.c_int32, _vp]
         lib.w4a16_autotune.restype = ctypes.c_int
+        lib.w4a16_gated_gemm.argtypes = [_vp] * 8 + [_i64] * 4 + [ctypes.c_int, ctypes.c_uint32, _vp]
+        lib.w4a16_gated_gemm.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -347,6 +351,12 @@ def w4a16_moe_static_scratch_bytes() -> int:
     return int(load().w4a16_moe_static_scratch_bytes())
 
 
+def w4a16_gated_gemm(A, Wt_gate, S_gate, Wt_up, S_up, H, Pg, Pu, M: int, N: int, K: int, G: int, act: int,
+                     flags: int = 0, stream=None) -> int:
+    return load().w4a16_gated_gemm(_addr(A), _addr(Wt_gate), _addr(S_gate), _addr(Wt_up), _addr(S_up), _addr(H),
+                                   _addr(Pg), _addr(Pu), M, N, K, G, act, flags, _stream(stream))
+
+
 def w4a16_gemm_launch_info(M: int, N: int, K: int, G: int):
     info = LaunchInfo()
     rc = load().w4a16_gemm_launch_info(M, N, K, G, ctypes.byref(info))
@@ -514,6 +524,82 @@ def gemm_w8(A, wt8, S, N: int, G: int, out=None, stream=None):
     C = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=A.device)
     _check(w8a16_gemm(A.contiguous(), wt8, S.contiguous(), C, M, N, K, G, stream), "w8a16_gemm")
     return C
+
+
+def _half_matrix(name: str, t, like=None, shape=None):
+    """A CUDA fp16 matrix operand, dense (a copy if it is not); `like`: the tensor whose device it must share."""
+    import torch
+    if not t.is_cuda or (like is not None and t.device != like.device):
+        raise ValueError(f"{name} must live on the same CUDA device as the other operands")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be float16")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be a matrix" + ("" if shape is None else f" of shape {list(shape)}")
+                         + f", got {list(t.shape)}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _weight_operand(name: str, wt, S, K: int, N: int, G: int, like):
+    """Tiled int4 weights [K, N] and their scales, checked for size; returns the dense scales."""
+    import torch
+    if wt.device != like.device:
+        raise ValueError(f"{name} must live on the same CUDA device as the other operands")
+    if G <= 0:
+        raise W4A16Error(ERR_INVALID_ARG, name)
+    if wt.dtype != torch.uint8 or wt.numel() != ((K + 63) // 64) * ((N + 127) // 128) * 4096 or not wt.is_contiguous():
+        raise ValueError(f"{name} must be the tiled layout of [{K}, {N}] codes (flat uint8)")
+    return _half_matrix(f"the scales of {name}", S, like, ((K + G - 1) // G, N))
+
+
+def _output(name: str, out, shape, like):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=torch.float16, device=like.device)
+    if out.device != like.device or out.dtype != torch.float16 or tuple(out.shape) != shape or not out.is_contiguous():
+        raise ValueError(f"{name} must be a dense float16 tensor of shape {list(shape)} on {like.device}")
+    return out
+
+
+class _on_device:
+    """Makes a tensor's device current for one call, if it is not already."""
+
+    def __init__(self, tensor):
+        import torch
+        index = tensor.device.index
+        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_SILU, save: bool = False, out=None,
+               out_gate=None, out_up=None, flags: int = 0, stream=None):
+    """H [M, N] fp16 = act(A x W_gate) * (A x W_up) from activations A [M, K] fp16 and two tiled weight
+    matrices [K, N] with scales [ceil(K/G), N]; one rounding. With save=True returns (H, gate, up), the two
+    projections in fp16 as gated_gemm_backward reads them."""
+    A = _half_matrix("A", A)
+    M, K = A.shape
+    S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, A)
+    S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, A)
+    H = _output("out", out, (M, N), A)
+    Pg = Pu = None
+    if save:
+        Pg, Pu = _output("out_gate", out_gate, (M, N), A), _output("out_up", out_up, (M, N), A)
+    if M == 0:  # (an empty tensor has no address to pass)
+        return (H, Pg, Pu) if save else H
+    with _on_device(A):
+        st = _current_stream(A.device.index) if stream is None else _stream(stream)
+        rc = (_lib or load()).w4a16_gated_gemm(A.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(), wt_up.data_ptr(),
+                                               S_up.data_ptr(), H.data_ptr(), _addr(Pg), _addr(Pu), M, N, K, G, act,
+                                               flags, st)
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_gated_gemm")
+    return (H, Pg, Pu) if save else H
 
 
 def device_status(clear: bool = True) -> int:

@@ -88,6 +88,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Barrier `id` (1..15) over `threads` threads of the CTA (whole warps).
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // ------------------------------------------------------------ async copies
 
 // 1-D bulk copy global -> this CTA's shared memory, completing on `bar`.

@@ -85,8 +85,19 @@ struct Params {
     int32_t vec_out;    // C rows start on 16-byte boundaries (16-byte output stores)
     long long wait_limit;   // bound of every device wait, in SM clock cycles
     int32_t stall_stage;    // test aid: the dequantising warps withhold this stage's ready signal (< 0: never)
-    int32_t act;            // W4A16_ACT_*: elementwise activation of the fp16 result (no K split)
+    int32_t act;            // W4A16_ACT_*: elementwise activation of the fp16 result (no K split); gated: the gate's
+    // Gated form: wt[0] / sc[0] are the gate's, wt[1] / sc[1] the up projection's; C
+    // is H, and Pg / Pu (both or neither) take the projections themselves.
+    __half* Pg;
+    __half* Pu;
 };
+
+// What a launch computes. kPlain: the dense or the grouped-expert product.
+// kGated: H = act(A W_gate) * (A W_up): a CTA owns 64 output columns, TMEM lanes
+// 0..63 hold their gate columns and lanes 64..127 the same up columns, so one
+// MMA sequence over one activation stream makes both projections, at the cost
+// of a dense product twice as wide; the epilogue pairs the two halves.
+enum GemmForm { kPlain = 0, kGated = 1 };
 
 // One ring of LS stages. Stage s owns, in shared memory, an activation tile
 // and, in tensor memory, a 32-column slot for the dequantised fp16 weights;
@@ -108,6 +119,7 @@ struct Layout {
     static_assert(TMEM_COLS == 32 || TMEM_COLS == 64 || TMEM_COLS == 128 || TMEM_COLS == 256 || TMEM_COLS == 512,
                   "TMEM allocations are powers of two");
     static_assert(kRedBytes <= kBar, "split-K buffer must fit in the activation ring");
+    static_assert(BN * kTileN * 3 <= kBar, "the gated epilogue's exchange and output tiles fit in the activation ring");
     static_assert((kActBytes % 1024) == 0, "activation tiles need 1024-byte alignment");
     static_assert((LS % 2) == 0, "the MMA thread takes the ring two stages at a time");
 };
@@ -182,11 +194,14 @@ __device__ __forceinline__ bool warp_drain_phase(uint64_t* bar, uint32_t parity)
 // BITS: 4 for the int4 tiled layout, 8 for the 8-bit code layout (W8A16): a
 // stage's tile is 4 or 8 KB, and a thread loads 2 or 4 16-byte chunks of its
 // column per stage; everything after the decode is the same.
-template <int BN, int LS, int TMEM_COLS, int MINB, int DQ, bool OG, int BITS>
+template <int BN, int LS, int TMEM_COLS, int MINB, int DQ, bool OG, int BITS, int FORM>
 __global__ void __launch_bounds__(threads_for(DQ), MINB)
     w4a16_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ Params p) {
     using L = Layout<BN, LS, TMEM_COLS>;
     static_assert(BITS == 4 || BITS == 8, "int4 or 8-bit codes");
+    constexpr bool GATED = FORM == kGated;
+    static_assert(!GATED || BITS == 4, "the gated form reads int4 codes");
+    constexpr int kCols = GATED ? kTileN / 2 : kTileN;  // output columns of a CTA
     constexpr int kTileBytes = BITS == 4 ? kRawBytes : 2 * kRawBytes;  // one 128 x 64 tile of codes
     constexpr int kChunks = BITS / 2;                                  // 16-byte chunks per column and stage
     constexpr int kScales = OG ? 1 : 8;  // scale registers per stage and thread
@@ -240,6 +255,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         tile_info[1] = expert;
         tile_info[2] = m0;
         tile_info[3] = rows;
+        tile_info[4] = 1;
     }
     __syncthreads();
     if (!tile_info[0]) return;  // grouped slot beyond the routed tiles (no cluster in that mode)
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
     const int grp = dw >> 2;          // dequantisation group: stages grp, grp + DQ, ...
     const int quad = warp & 3;        // TMEM lane quadrant this warp may access
     const int j = quad * 32 + lane;   // weight column inside the tile = TMEM lane
-    const int n = nt * kTileN + j;
+    const int n = GATED ? nt * kCols + (j & (kCols - 1)) : nt * kTileN + j;
     const bool col_ok = n < p.N;
     const uint32_t tlane = static_cast<uint32_t>(quad * 32) << 16;
     // Codes and scales of this thread's stages (i = grp, grp + DQ, ...) are
@@ -277,8 +293,13 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
     // that reads a register whose load is in flight waits for that load.
     // kk is the first k of the next stage to load, gk = floor(kk / G).
     // (A padded column past N reads column 0's scales; its codes are 0.)
-    const uint8_t* wcol = p.wt[expert] + static_cast<int64_t>(nt) * p.KT * kTileBytes + j * 16;
-    const __half* scol = p.sc[expert] + (col_ok ? n : 0);
+    // (Gated: the lane's half picks the matrix, and a CTA's 64 columns are one half of a 128-column weight tile.)
+    const int half = GATED ? j / kCols : 0;
+    const int wtile_n = GATED ? nt >> 1 : nt;
+    const int wtile_j = GATED ? (nt & 1) * kCols + (j & (kCols - 1)) : j;
+    const uint8_t* wcol =
+        p.wt[GATED ? half : expert] + static_cast<int64_t>(wtile_n) * p.KT * kTileBytes + wtile_j * 16;
+    const __half* scol = p.sc[GATED ? half : expert] + (col_ok ? n : 0);
     int li = grp;
     int kk = (kb + grp) * kTileK;
     int gk = kk / p.G;
@@ -351,7 +372,10 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
             // L2 kPrefetchStages ahead, so that the dequantising threads' own
             // loads (issued only kAhead of their stages ahead) find it there.
             // (The ring's first LS activation tiles go out before the prefetches.)
-            const uint8_t* wtile = p.wt[expert] + (static_cast<int64_t>(nt) * p.KT + kb) * kTileBytes;
+            // (Gated: two neighbouring CTAs read the same two tiles; the even one fetches the gate's, the odd
+            // one the up projection's.)
+            const uint8_t* wtile =
+                p.wt[GATED ? nt & 1 : expert] + (static_cast<int64_t>(GATED ? nt >> 1 : nt) * p.KT + kb) * kTileBytes;
             const int first = min(nst, LS);
             for (int i = 0; i < first; ++i) issue_act(i);
             for (int i = 0; i < min(nst, kPrefetchStages + first); ++i)
@@ -479,9 +503,59 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         tc_fence_after_sync();
         grid_dependency_wait();  // the output may still be read by the previous kernel
         const int aborted = __shfl_sync(0xffffffffu, *abort_flag, 0);
-        const bool have_acc = drained && !aborted && nst > 0;
-        if (dw == 0 && lane == 0) tile_info[4] = have_acc ? 1 : 0;
-        if (p.splits == 1) {
+        bool have_acc = drained && !aborted && nst > 0;
+        if constexpr (GATED) {
+            // The epilogue's barriers need one answer for every warp: the tile is
+            // written only if each of them found it complete.
+            if (lane == 0 && !have_acc) tile_info[4] = 0;
+            named_barrier(1 + DQ, kGroupWarps * 32 * DQ);
+            have_acc = tile_info[4] != 0;
+        } else {
+            if (dw == 0 && lane == 0) tile_info[4] = have_acc ? 1 : 0;
+        }
+        if (GATED && p.splits == 1) {
+            // Pair the halves: of each 16-token chunk a gate lane hands over its last
+            // eight tokens and keeps the first eight, an up lane the other way round,
+            // through an fp32 tile [token][64 columns] in the idle activation ring.
+            // Each then owns both projections of eight outputs of its column. The
+            // projections to keep are staged afterwards, over the exchange tile.
+            if (have_acc) {
+                float* xch = reinterpret_cast<float*>(smem + L::kAct);
+                __half* htile = reinterpret_cast<__half*>(smem + L::kAct + BN * kCols * 4);
+                const int jc = j & (kCols - 1);
+                const int keep = half ? 8 : 0, give = 8 - keep;
+                const int nch = n_mma / 16;
+                for (int c = grp; c < nch; c += DQ) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(tmem_acc + tlane + c * 16, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        xch[(c * 16 + give + t) * kCols + jc] = __uint_as_float(half ? v[t] : v[8 + t]);
+                    named_barrier(1 + grp, kGroupWarps * 32);  // (the chunk's four warps: both halves of its 64 columns)
+                    const int act = p.act;
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const float mine = __uint_as_float(half ? v[8 + t] : v[t]);
+                        const float other = xch[(c * 16 + keep + t) * kCols + jc];
+                        const float h = half ? gate_value(other, act) * mine : gate_value(mine, act) * other;
+                        htile[(c * 16 + keep + t) * kCols + jc] = __float2half_rn(h);
+                    }
+                }
+                if (p.Pg) {
+                    named_barrier(1 + DQ, kGroupWarps * 32 * DQ);  // every thread is done with the exchange tile
+                    __half* ptile = reinterpret_cast<__half*>(smem + L::kAct);  // [token][gate 64 | up 64]
+                    for (int c = grp; c < nch; c += DQ) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(tmem_acc + tlane + c * 16, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int t = 0; t < 16; ++t)
+                            ptile[(c * 16 + t) * kTileN + j] = __float2half_rn(__uint_as_float(v[t]));
+                    }
+                }
+            }
+        } else if (p.splits == 1) {
             // Stage the fp16 tile, row-major [token][128 columns], in the idle
             // activation ring (every copy into it was consumed by a completed
             // MMA), so that the global stores below are whole 16-byte vectors.
@@ -539,7 +613,30 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         tmem_dealloc(tmem_acc, TMEM_COLS);
     }
 
-    if (p.splits == 1 && tile_info[4]) {
+    if (GATED && p.splits == 1 && tile_info[4]) {
+        // Rows of 64 columns, 8 chunks of 16 bytes each: H, then the projections.
+        const int n0 = nt * kCols;
+        auto store_rows = [&](const __half* tile, int stride, __half* out) {
+            for (int o = threadIdx.x; o < rows * 8; o += static_cast<int>(blockDim.x)) {
+                const int r = o >> 3;
+                const int cc = (o & 7) * 8;
+                __half* dst = out + static_cast<int64_t>(m0 + r) * p.N + n0 + cc;
+                if (p.vec_out && n0 + cc + 8 <= p.N) {
+                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(tile + r * stride + cc);
+                } else {
+                    for (int e = 0; e < 8 && n0 + cc + e < p.N; ++e) dst[e] = tile[r * stride + cc + e];
+                }
+            }
+        };
+        store_rows(reinterpret_cast<const __half*>(smem + L::kAct + BN * kCols * 4), kCols, p.C);
+        if (p.Pg) {
+            const __half* ptile = reinterpret_cast<const __half*>(smem + L::kAct);
+            store_rows(ptile, kTileN, p.Pg);
+            store_rows(ptile + kCols, kTileN, p.Pu);
+        }
+    }
+
+    if (!GATED && p.splits == 1 && tile_info[4]) {
         // Row r of the tile is 16 chunks of 8 columns; a warp writes two rows
         // per instruction.
         const __half* stile = reinterpret_cast<const __half*>(smem + L::kAct);
@@ -561,7 +658,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         // [r*128/S, (r+1)*128/S) of the tile.
         cluster_sync_all();
         const int S = p.splits;
-        const int cw = kTileN / S;
+        const int cw = kCols / S;
         const int rank = static_cast<int>(cluster_ctarank());
         const float* red = reinterpret_cast<const float*>(smem + L::kAct);
         // A CTA that stopped early left its partial tile incomplete: if any CTA of
@@ -572,16 +669,38 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         for (int o = threadIdx.x; o < cw * rows; o += static_cast<int>(blockDim.x)) {
             const int col = rank * cw + (o % cw);
             const int tok = o / cw;
-            const int nn = nt * kTileN + col;
+            const int nn = nt * kCols + col;
             if (nn < p.N && !aborted) {
-                float part[8];
+                if constexpr (GATED) {
+                    float gate[8], up[8];
 #pragma unroll
-                for (int src = 0; src < 8; ++src)
-                    part[src] = src < S ? ld_dsmem_f32(&red[tok * kTileN + col], static_cast<uint32_t>(src)) : 0.f;
-                float acc = 0.f;
+                    for (int src = 0; src < 8; ++src) {
+                        const bool in = src < S;
+                        gate[src] = in ? ld_dsmem_f32(&red[tok * kTileN + col], static_cast<uint32_t>(src)) : 0.f;
+                        up[src] = in ? ld_dsmem_f32(&red[tok * kTileN + kCols + col], static_cast<uint32_t>(src)) : 0.f;
+                    }
+                    float gv = 0.f, uv = 0.f;
 #pragma unroll
-                for (int src = 0; src < 8; ++src) acc += part[src];  // rank order
-                p.C[static_cast<int64_t>(m0 + tok) * p.N + nn] = __float2half_rn(acc);
+                    for (int src = 0; src < 8; ++src) {  // rank order
+                        gv += gate[src];
+                        uv += up[src];
+                    }
+                    const int64_t o2 = static_cast<int64_t>(m0 + tok) * p.N + nn;
+                    p.C[o2] = __float2half_rn(gate_value(gv, p.act) * uv);
+                    if (p.Pg) {
+                        p.Pg[o2] = __float2half_rn(gv);
+                        p.Pu[o2] = __float2half_rn(uv);
+                    }
+                } else {
+                    float part[8];
+#pragma unroll
+                    for (int src = 0; src < 8; ++src)
+                        part[src] = src < S ? ld_dsmem_f32(&red[tok * kTileN + col], static_cast<uint32_t>(src)) : 0.f;
+                    float acc = 0.f;
+#pragma unroll
+                    for (int src = 0; src < 8; ++src) acc += part[src];  // rank order
+                    p.C[static_cast<int64_t>(m0 + tok) * p.N + nn] = __float2half_rn(acc);
+                }
             }
         }
         cluster_sync_all();
@@ -610,19 +729,21 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+enum Kind { kInt4 = 0, kInt8 = 1, kGatedInt4 = 2, kKinds = 3 };
+
 struct Variant {
     int bn;
     int threads;
     int nominal_per_sm;  // the residency the variant is sized for (used when no device is present)
     int tmem_cols;       // TMEM columns each resident CTA allocates
     int smem;
-    // [2 * (8-bit codes) + (any G)]: forms for int4 / 8-bit codes, with G a multiple
-    // of 64 (one scale per stage) or any G
-    const void* fn[4];
-    int (*launch[4])(const CUtensorMap&, const Params&, dim3, int, int, cudaStream_t);
+    // [2 * kind + (any G)]: the product with int4 codes (kind 0) and 8-bit codes (1)
+    // and the gated form (2), with G a multiple of 64 (one scale per stage) or any G
+    const void* fn[2 * kKinds];
+    int (*launch[2 * kKinds])(const CUtensorMap&, const Params&, dim3, int, int, cudaStream_t);
 };
 
-template <int BN, int LS, int TC, int MINB, int DQ, bool OG, int BITS>
+template <int BN, int LS, int TC, int MINB, int DQ, bool OG, int BITS, int FORM>
 int launch_variant(const CUtensorMap& map, const Params& p, dim3 grid, int cluster_x, int smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -643,7 +764,7 @@ int launch_variant(const CUtensorMap& map, const Params& p, dim3 grid, int clust
     }
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, OG, BITS>, map, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, OG, BITS, FORM>, map, p);
     return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
 }
 
@@ -654,12 +775,18 @@ Variant make_variant() {
                    MINB,
                    TC,
                    Layout<BN, LS, TC>::kAlloc,
-                   {reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 4>),
-                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 4>),
-                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 8>),
-                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 8>)},
-                   {&launch_variant<BN, LS, TC, MINB, DQ, true, 4>, &launch_variant<BN, LS, TC, MINB, DQ, false, 4>,
-                    &launch_variant<BN, LS, TC, MINB, DQ, true, 8>, &launch_variant<BN, LS, TC, MINB, DQ, false, 8>}};
+                   {reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 4, kPlain>),
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 4, kPlain>),
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 8, kPlain>),
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 8, kPlain>),
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 4, kGated>),
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 4, kGated>)},
+                   {&launch_variant<BN, LS, TC, MINB, DQ, true, 4, kPlain>,
+                    &launch_variant<BN, LS, TC, MINB, DQ, false, 4, kPlain>,
+                    &launch_variant<BN, LS, TC, MINB, DQ, true, 8, kPlain>,
+                    &launch_variant<BN, LS, TC, MINB, DQ, false, 8, kPlain>,
+                    &launch_variant<BN, LS, TC, MINB, DQ, true, 4, kGated>,
+                    &launch_variant<BN, LS, TC, MINB, DQ, false, 4, kGated>}};
 }
 
 // Token tiles and their pipeline depths: small tiles keep two CTAs per SM; the
@@ -683,7 +810,7 @@ const Variant& variant_for(int bn) {
 
 struct DeviceState {
     bool ready = false;
-    int ctas_per_sm[2][kNumVariants] = {};  // [8-bit codes][variant]
+    int ctas_per_sm[kKinds][kNumVariants] = {};
 };
 
 int prepare_device(DeviceState** out) {
@@ -694,11 +821,11 @@ int prepare_device(DeviceState** out) {
     std::lock_guard<std::mutex> lock(mu);
     DeviceState& st = states[dev];
     if (!st.ready) {
-        for (int i = 0; i < 2 * kNumVariants; ++i) {
+        for (int i = 0; i < kKinds * kNumVariants; ++i) {
             const Variant& v = kVariants[i % kNumVariants];
-            const int b8 = i / kNumVariants;
+            const int kind = i / kNumVariants;
             int n = 1 << 30;
-            for (int f = 2 * b8; f < 2 * b8 + 2; ++f) {
+            for (int f = 2 * kind; f < 2 * kind + 2; ++f) {
                 const void* fn = v.fn[f];
                 if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess ||
                     cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -721,7 +848,7 @@ int prepare_device(DeviceState** out) {
                 n = std::min(n, 512 / v.tmem_cols);  // every resident CTA holds its TMEM columns
             }
             if (n < 1) return W4A16_ERR_UNSUPPORTED;
-            st.ctas_per_sm[b8][i % kNumVariants] = n;
+            st.ctas_per_sm[kind][i % kNumVariants] = n;
         }
         st.ready = true;
     }
@@ -763,7 +890,7 @@ struct Plan {
 // split only with a single token tile, a power of two that leaves every
 // cluster rank at least two K stages); 0 takes the heuristic.
 int plan_dense(int64_t M, int64_t N, int64_t K, Plan* plan, bool need_device, int bn_force = 0,
-               int splits_force = 0, int bits = 4) {
+               int splits_force = 0, Kind kind = kInt4) {
     const int bn = bn_force > 0 ? bn_force : token_tile_for(M);
     if (variant_for(bn).bn != bn) return W4A16_ERR_UNSUPPORTED;
     const int vi = variant_index(bn);
@@ -772,10 +899,11 @@ int plan_dense(int64_t M, int64_t N, int64_t K, Plan* plan, bool need_device, in
         DeviceState* st = nullptr;
         int rc = prepare_device(&st);
         if (rc) return rc;
-        per_sm = st->ctas_per_sm[bits == 8 ? 1 : 0][vi];
+        per_sm = st->ctas_per_sm[kind][vi];
         sms = sm_count();
     }
-    const int64_t NT = (N + kTileN - 1) / kTileN;
+    const int cols = kind == kGatedInt4 ? kTileN / 2 : kTileN;  // output columns of a CTA
+    const int64_t NT = (N + cols - 1) / cols;
     const int64_t MT = (M + bn - 1) / bn;
     const int64_t KT = (K + kTileK - 1) / kTileK;
     if (NT > 65535 || MT > 65535) return W4A16_ERR_UNSUPPORTED;
@@ -809,7 +937,7 @@ int plan_grouped(int64_t E, int64_t total_rows, int64_t N, int64_t K, Plan* plan
         DeviceState* st = nullptr;
         int rc = prepare_device(&st);
         if (rc) return rc;
-        per_sm = st->ctas_per_sm[0][vi];
+        per_sm = st->ctas_per_sm[kInt4][vi];
     }
     const int64_t NT = (N + kTileN - 1) / kTileN;
     const int64_t slots = total_rows / bn + E;  // >= sum over experts of ceil(rows_e / bn)
@@ -965,6 +1093,19 @@ int dense_launch(const Plan& plan, int bits, const w4a16_half* A_dev, const uint
                  const w4a16_half* S_dev, w4a16_half* C_dev, int64_t M, int64_t N, int64_t K, int64_t G,
                  cudaStream_t stream);
 
+int encode_activation_map(CUtensorMap* map, const void* A, int64_t rows, int64_t K, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return W4A16_ERR_CUDA;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(kTileK), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(A), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? W4A16_OK : W4A16_ERR_CUDA;
+}
+
 int activation_map(CUtensorMap* map, const void* A, int64_t rows, int64_t K, int box_rows) {
     // A small per-thread cache: the encoder costs more than the rest of a
     // decode-sized call on the host, and the same activation buffers recur.
@@ -986,16 +1127,8 @@ int activation_map(CUtensorMap* map, const void* A, int64_t rows, int64_t K, int
             return W4A16_OK;
         }
     }
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return W4A16_ERR_CUDA;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(kTileK), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(A), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return W4A16_ERR_CUDA;
+    const int rc = encode_activation_map(map, A, rows, K, box_rows);
+    if (rc) return rc;
     Entry& e = cache[next];
     e.A = A;
     e.rows = rows;
@@ -1050,8 +1183,13 @@ std::atomic<long long> g_wait_limit{kTimeoutCycles};  // test aid: w4a16_set_fau
 std::atomic<int> g_stall_stage{-1};
 }
 
-// Set by w4a16_gemm_ex for the duration of one call on this host thread.
+// Set by the entry points with per-call flags for the duration of one call on this host thread.
 thread_local int t_call_static_weights = 0;
+
+struct CallStaticWeights {
+    explicit CallStaticWeights(bool on) { t_call_static_weights = on ? 1 : 0; }
+    ~CallStaticWeights() { t_call_static_weights = 0; }
+};
 
 bool static_weights_enabled() {
     return t_call_static_weights != 0 || g_static_weights.load(std::memory_order_relaxed) != 0;
@@ -1249,6 +1387,76 @@ int grouped_gemm_act(const w4a16_half* A_dev, const uint8_t* const* Wt, const w4
 
 }  // namespace w4a16
 
+namespace w4a16 {
+namespace {
+
+int gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate, const w4a16_half* S_gate, const uint8_t* Wt_up,
+               const w4a16_half* S_up, w4a16_half* H_dev, w4a16_half* Pg_dev, w4a16_half* Pu_dev, int64_t M, int64_t N,
+               int64_t K, int64_t G, int act, cudaStream_t stream) {
+    SkinnyPlan sk;
+    if (skinny_plan_gated(M, N, K, G, &sk) == W4A16_OK)
+        return skinny_gated_launch(sk, A_dev, Wt_gate, S_gate, Wt_up, S_up, H_dev, Pg_dev, Pu_dev, M, N, K, G, act,
+                                   stream);
+    Plan plan;
+    int rc = plan_dense(M, N, K, &plan, true, 0, 0, kGatedInt4);
+    if (rc) return rc;
+    Params p;
+    std::memset(&p, 0, sizeof(p));
+    p.wt[0] = Wt_gate;
+    p.wt[1] = Wt_up;
+    p.sc[0] = reinterpret_cast<const __half*>(S_gate);
+    p.sc[1] = reinterpret_cast<const __half*>(S_up);
+    p.C = reinterpret_cast<__half*>(H_dev);
+    p.Pg = reinterpret_cast<__half*>(Pg_dev);
+    p.Pu = reinterpret_cast<__half*>(Pu_dev);
+    p.rows = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.G = static_cast<int32_t>(G);
+    p.ngroups = static_cast<int32_t>((K + G - 1) / G);
+    p.KT = static_cast<int32_t>((K + kTileK - 1) / kTileK);
+    p.E = 1;
+    p.splits = plan.splits;
+    p.act = act;
+    p.prefetch = static_weights_enabled() ? 1 : 0;
+    p.vec_out = aligned16(H_dev) && aligned16(Pg_dev) && aligned16(Pu_dev);
+    p.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+    p.stall_stage = g_stall_stage.load(std::memory_order_relaxed);
+    CUtensorMap map;
+    rc = encode_activation_map(&map, A_dev, M, K, plan.bn);
+    if (rc) return rc;
+    const Variant& v = variant_for(plan.bn);
+    return v.launch[2 * kGatedInt4 + ((G % kTileK) ? 1 : 0)](map, p, plan.grid, plan.splits, v.smem, stream);
+}
+
+}  // namespace
+}  // namespace w4a16
+
+extern "C" int w4a16_gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate_dev, const w4a16_half* S_gate_dev,
+                                const uint8_t* Wt_up_dev, const w4a16_half* S_up_dev, w4a16_half* H_dev,
+                                w4a16_half* Pg_dev, w4a16_half* Pu_dev, int64_t M, int64_t N, int64_t K, int64_t G,
+                                int act, uint32_t flags, void* stream) {
+    if (!A_dev || !Wt_gate_dev || !S_gate_dev || !Wt_up_dev || !S_up_dev || !H_dev || M < 0)
+        return W4A16_ERR_INVALID_ARG;
+    if ((Pg_dev == nullptr) != (Pu_dev == nullptr)) return W4A16_ERR_INVALID_ARG;
+    if (act < W4A16_ACT_IDENTITY || act > W4A16_ACT_SILU) return W4A16_ERR_INVALID_ARG;
+    if (flags & ~static_cast<uint32_t>(W4A16_FLAG_STATIC_WEIGHTS)) return W4A16_ERR_INVALID_ARG;
+    int rc = check_shape(N, K, G);
+    if (rc) return rc;
+    if (M >= (int64_t(1) << 31)) return W4A16_ERR_UNSUPPORTED;
+    if (!aligned16(A_dev) || !aligned16(Wt_gate_dev) || !aligned16(S_gate_dev) || !aligned16(Wt_up_dev) ||
+        !aligned16(S_up_dev) ||
+        ((reinterpret_cast<uintptr_t>(H_dev) | reinterpret_cast<uintptr_t>(Pg_dev) |
+          reinterpret_cast<uintptr_t>(Pu_dev)) & 1u))
+        return W4A16_ERR_MISALIGNED;
+    if (M == 0) return W4A16_OK;
+    rc = check_device();
+    if (rc) return rc;
+    const CallStaticWeights scope((flags & W4A16_FLAG_STATIC_WEIGHTS) != 0);
+    return gated_gemm(A_dev, Wt_gate_dev, S_gate_dev, Wt_up_dev, S_up_dev, H_dev, Pg_dev, Pu_dev, M, N, K, G, act,
+                      static_cast<cudaStream_t>(stream));
+}
+
 extern "C" int w4a16_grouped_gemm(const w4a16_half* A_dev, const uint8_t* const* Wt, const w4a16_half* const* S,
                                   const int32_t* offsets_dev, w4a16_half* C_dev, int64_t E, int64_t total_rows,
                                   int64_t N, int64_t K, int64_t G, void* stream) {
@@ -1441,7 +1649,7 @@ extern "C" int w8a16_gemm_launch_info(int64_t M, int64_t N, int64_t K, int64_t G
     if (rc) return rc;
     if (M >= (int64_t(1) << 31)) return W4A16_ERR_UNSUPPORTED;
     Plan plan;
-    rc = plan_dense(M, N, K, &plan, check_device() == W4A16_OK, 0, 0, 8);
+    rc = plan_dense(M, N, K, &plan, check_device() == W4A16_OK, 0, 0, kInt8);
     if (rc) return rc;
     fill_info(plan, info);
     return W4A16_OK;
@@ -1460,7 +1668,7 @@ extern "C" int w8a16_gemm(const w4a16_half* A_dev, const uint8_t* Wt8_dev, const
     rc = check_device();
     if (rc) return rc;
     Plan plan;
-    rc = plan_dense(M, N, K, &plan, true, 0, 0, 8);
+    rc = plan_dense(M, N, K, &plan, true, 0, 0, kInt8);
     if (rc) return rc;
     return dense_launch(plan, 8, A_dev, Wt8_dev, S_dev, C_dev, M, N, K, G, static_cast<cudaStream_t>(stream));
 }
@@ -1469,9 +1677,6 @@ extern "C" int w4a16_gemm_ex(const w4a16_half* A_dev, const uint8_t* Wt_dev, con
                              w4a16_half* C_dev, int64_t M, int64_t N, int64_t K, int64_t G, uint32_t flags,
                              void* stream) {
     if (flags & ~static_cast<uint32_t>(W4A16_FLAG_STATIC_WEIGHTS)) return W4A16_ERR_INVALID_ARG;
-    struct CallScope {
-        explicit CallScope(int v) { t_call_static_weights = v; }
-        ~CallScope() { t_call_static_weights = 0; }
-    } scope((flags & W4A16_FLAG_STATIC_WEIGHTS) ? 1 : 0);
+    const CallStaticWeights scope((flags & W4A16_FLAG_STATIC_WEIGHTS) != 0);
     return w4a16_gemm(A_dev, Wt_dev, S_dev, C_dev, M, N, K, G, stream);
 }

@@ -31,6 +31,8 @@ int make_half_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_
 // kernels stage them. Encoded maps are kept in a small per-thread cache keyed
 // by (device, address, rows, K, box_rows), so repeated calls on the same
 // buffers skip the encoder.
+// encode_activation_map is the encoder alone.
+int encode_activation_map(CUtensorMap* map, const void* A, int64_t rows, int64_t K, int box_rows);
 int activation_map(CUtensorMap* map, const void* A, int64_t rows, int64_t K, int box_rows);
 
 // The grouped-expert GEMM with an activation epilogue (w4a16_grouped_gemm_act).
@@ -78,6 +80,13 @@ int skinny_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt, cons
 // The skinny plan of the grouped form: the smallest K split whose staged
 // activations fit (the experts' column tiles already fill the grid).
 int skinny_plan_grouped(int64_t total_rows, int64_t N, int64_t K, int64_t G, SkinnyPlan* plan);
+
+// The skinny plan and launch of the gated projections (M <= kSkinnyMaxM): H
+// [M, N], and the projections Pg and Pu if not null.
+int skinny_plan_gated(int64_t M, int64_t N, int64_t K, int64_t G, SkinnyPlan* plan);
+int skinny_gated_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt_gate, const void* S_gate,
+                        const uint8_t* Wt_up, const void* S_up, void* H, void* Pg, void* Pu, int64_t M, int64_t N,
+                        int64_t K, int64_t G, int act, cudaStream_t stream);
 
 // Grouped-expert form of the skinny kernel (grid z = expert) for at most 16
 // gathered rows in total (plan from skinny_plan_grouped): rows
