@@ -313,6 +313,30 @@ int w4a16_gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate_dev, const 
                      w4a16_half* Pu_dev, int64_t M, int64_t N, int64_t K, int64_t G, int act, uint32_t flags,
                      void* stream);
 
+/* The product with the transposed weights, the gradient of w4a16_gemm's input:
+ * dA_dev [M, K] = fp16(sum_n dC[m, n] * W[k, n]) from dC_dev [M, N]. The weights
+ * are the same tiled layout and scales as the forward product's; no transposed
+ * copy is needed. flags as for w4a16_gated_gemm. Contract of w4a16_gemm with
+ * dC_dev in the place of A_dev and dA_dev in that of C_dev. M == 0 is a no-op.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, CUDA. */
+int w4a16_gemm_dgrad(const w4a16_half* dC_dev, const uint8_t* Wt_dev, const w4a16_half* S_dev, w4a16_half* dA_dev,
+                     int64_t M, int64_t N, int64_t K, int64_t G, uint32_t flags, void* stream);
+
+/* Backward pass of w4a16_gated_gemm with frozen weights, from the gradient
+ * dH_dev [M, N] and the kept projections Pg_dev, Pu_dev [M, N]:
+ *     dPg = fp16(dH * Pu * act'(Pg)),   dPu = fp16(dH * act(Pg)),
+ *     dA  = fp16(dPg W_gate^T + dPu W_up^T)      (one fp32 sum over both),
+ * all three written: dPg_dev and dPu_dev [M, N] are what gradients of adapters
+ * on the projections need, dA_dev [M, K] goes on to the layer below. relu'(0) =
+ * 0. No output may overlap an input or another output. All [M, N] matrices,
+ * weights and scales 16-byte aligned, dA 2-byte aligned; flags and the rest as
+ * for w4a16_gated_gemm. Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, CUDA. */
+int w4a16_gated_gemm_backward(const w4a16_half* dH_dev, const w4a16_half* Pg_dev, const w4a16_half* Pu_dev,
+                              const uint8_t* Wt_gate_dev, const w4a16_half* S_gate_dev, const uint8_t* Wt_up_dev,
+                              const w4a16_half* S_up_dev, w4a16_half* dPg_dev, w4a16_half* dPu_dev,
+                              w4a16_half* dA_dev, int64_t M, int64_t N, int64_t K, int64_t G, int act,
+                              uint32_t flags, void* stream);
+
 /* Declares (enable != 0) or withdraws (enable == 0) the promise that no
  * kernel on the calling streams writes the tiled weights or the scales passed
  * to w4a16_gemm right before that call, i.e. the weights are static (prepared

@@ -89,3 +89,23 @@ def worst(got: np.ndarray, ref: np.ndarray, bound: np.ndarray) -> float:
     """The largest error in units of its bound (below 1 everywhere if the result is right)."""
     err = np.abs(got.astype(np.float64) - ref)
     return float(np.max(err / bound, initial=0.0)) if np.all(np.isfinite(got)) else float("inf")
+
+
+def slopes(dH, g, u, a):
+    """(dG, dU) of the gated product from fp16 projections, and the bounds of their fp16 results' errors."""
+    dH, g, u = (x.astype(np.float64) for x in (dH, g, u))
+    d, v = slope(g, a), act(g, a)
+    # evaluation: 2^-18 of the derivative's terms (none above 1.2, or of act's); three fp32 products
+    ed = 2.0 ** -18 * np.maximum(np.abs(d), 2.0 ** -4)
+    ev = 2.0 ** -18 * np.maximum(np.abs(v), np.minimum(np.abs(g), 1.0) * 2.0 ** -4)
+    dG, dU = dH * u * d, dH * v
+    return (dG, dU), (half_step(dG) + np.abs(dH * u) * ed, half_step(dU) + np.abs(dH) * ev)
+
+
+def gated_backward(dH, g, u, Wg, Wu, a):
+    """(dA, dG, dU) and their bounds; dA's counts the rounding of dG and dU to fp16 before their products."""
+    (dG, dU), (eG, eU) = slopes(dH, g, u, a)
+    dA = dG @ Wg.T + dU @ Wu.T
+    T = np.abs(dG) @ np.abs(Wg).T + np.abs(dU) @ np.abs(Wu).T
+    eA = sum_error(2 * Wg.shape[1], T) + eG @ np.abs(Wg).T + eU @ np.abs(Wu).T
+    return (dA, dG, dU), (half_step(dA) + 1.001 * eA, eG, eU)

@@ -29,3 +29,31 @@ def test_gated_gemm_rejects_bad_arguments_on_host():
     assert g(H=FAKE + 1) == w.ERR_MISALIGNED
     assert g(Pg=FAKE + 1, Pu=FAKE) == w.ERR_MISALIGNED
     assert g(M=0) == w.OK and g(M=0, Pg=FAKE, Pu=FAKE) == w.OK
+
+
+def test_dgrad_rejects_bad_arguments_on_host():
+    def g(dC=FAKE, wt=FAKE, s=FAKE, dA=FAKE, M=4, N=128, K=128, G=64, flags=0):
+        return w.w4a16_gemm_dgrad(dC, wt, s, dA, M, N, K, G, flags, stream=0)
+    for name in ("dC", "wt", "s", "dA"):
+        assert g(**{name: None}) == w.ERR_INVALID_ARG, name
+    assert g(M=-1) == w.ERR_INVALID_ARG and g(K=0) == w.ERR_INVALID_ARG and g(flags=4) == w.ERR_INVALID_ARG
+    assert g(N=100) == w.ERR_UNSUPPORTED and g(K=100) == w.ERR_UNSUPPORTED and g(G=24) == w.ERR_UNSUPPORTED
+    for name in ("dC", "wt", "s"):
+        assert g(**{name: FAKE + 8}) == w.ERR_MISALIGNED, name
+    assert g(dA=FAKE + 1) == w.ERR_MISALIGNED
+    assert g(M=0) == w.OK
+
+
+def test_gated_backward_rejects_bad_arguments_on_host():
+    names = ("dH", "Pg", "Pu", "wg", "sg", "wu", "su", "dPg", "dPu", "dA")
+
+    def g(M=4, N=128, K=128, G=64, act=w.ACT_SILU, flags=0, **kw):
+        return w.w4a16_gated_gemm_backward(*[kw.get(n, FAKE) for n in names], M, N, K, G, act, flags, stream=0)
+    for name in names:
+        assert g(**{name: None}) == w.ERR_INVALID_ARG, name
+    for name in names[:-1]:
+        assert g(**{name: FAKE + 8}) == w.ERR_MISALIGNED, name
+    assert g(dA=FAKE + 1) == w.ERR_MISALIGNED
+    assert g(act=5) == w.ERR_INVALID_ARG and g(flags=2) == w.ERR_INVALID_ARG and g(M=-1) == w.ERR_INVALID_ARG
+    assert g(N=100) == w.ERR_UNSUPPORTED and g(K=100) == w.ERR_UNSUPPORTED and g(G=24) == w.ERR_UNSUPPORTED
+    assert g(M=0) == w.OK

@@ -43,7 +43,7 @@ EXPORTED = [
     "w4a16_set_tactic", "w4a16_get_tactic", "w4a16_clear_tactics", "w4a16_autotune",
     "w8a16_tiled_bytes", "w8a16_repack", "w8a16_gemm", "w8a16_gemm_launch_info",
     "w4a16_moe_layer_static", "w4a16_moe_static_scratch_bytes", "w4a16_gemm_ex", "w8a16_quantize",
-    "w4a16_gated_gemm",
+    "w4a16_gated_gemm", "w4a16_gemm_dgrad", "w4a16_gated_gemm_backward",
 ]
 
 
@@ -152,6 +152,10 @@ def load() -> ctypes.CDLL:
         lib.w4a16_autotune.restype = ctypes.c_int
         lib.w4a16_gated_gemm.argtypes = [_vp] * 8 + [_i64] * 4 + [ctypes.c_int, ctypes.c_uint32, _vp]
         lib.w4a16_gated_gemm.restype = ctypes.c_int
+        lib.w4a16_gemm_dgrad.argtypes = [_vp] * 4 + [_i64] * 4 + [ctypes.c_uint32, _vp]
+        lib.w4a16_gemm_dgrad.restype = ctypes.c_int
+        lib.w4a16_gated_gemm_backward.argtypes = [_vp] * 10 + [_i64] * 4 + [ctypes.c_int, ctypes.c_uint32, _vp]
+        lib.w4a16_gated_gemm_backward.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -355,6 +359,17 @@ def w4a16_gated_gemm(A, Wt_gate, S_gate, Wt_up, S_up, H, Pg, Pu, M: int, N: int,
                      flags: int = 0, stream=None) -> int:
     return load().w4a16_gated_gemm(_addr(A), _addr(Wt_gate), _addr(S_gate), _addr(Wt_up), _addr(S_up), _addr(H),
                                    _addr(Pg), _addr(Pu), M, N, K, G, act, flags, _stream(stream))
+
+
+def w4a16_gemm_dgrad(dC, Wt, S, dA, M: int, N: int, K: int, G: int, flags: int = 0, stream=None) -> int:
+    return load().w4a16_gemm_dgrad(_addr(dC), _addr(Wt), _addr(S), _addr(dA), M, N, K, G, flags, _stream(stream))
+
+
+def w4a16_gated_gemm_backward(dH, Pg, Pu, Wt_gate, S_gate, Wt_up, S_up, dPg, dPu, dA, M: int, N: int, K: int, G: int,
+                              act: int, flags: int = 0, stream=None) -> int:
+    return load().w4a16_gated_gemm_backward(_addr(dH), _addr(Pg), _addr(Pu), _addr(Wt_gate), _addr(S_gate),
+                                            _addr(Wt_up), _addr(S_up), _addr(dPg), _addr(dPu), _addr(dA), M, N, K,
+                                            G, act, flags, _stream(stream))
 
 
 def w4a16_gemm_launch_info(M: int, N: int, K: int, G: int):
@@ -600,6 +615,47 @@ def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_S
     if rc != OK:
         raise W4A16Error(rc, "w4a16_gated_gemm")
     return (H, Pg, Pu) if save else H
+
+
+def gemm_dgrad(dC, wt, S, K: int, G: int, out=None, flags: int = 0, stream=None):
+    """dA [M, K] fp16 = dC [M, N] x W^T, the gradient of gemm's input, from the forward product's tiled weights
+    and scales [ceil(K/G), N]."""
+    dC = _half_matrix("dC", dC)
+    M, N = dC.shape
+    S = _weight_operand("wt", wt, S, K, N, G, dC)
+    dA = _output("out", out, (M, K), dC)
+    if M == 0:
+        return dA
+    with _on_device(dC):
+        st = _current_stream(dC.device.index) if stream is None else _stream(stream)
+        rc = (_lib or load()).w4a16_gemm_dgrad(dC.data_ptr(), wt.data_ptr(), S.data_ptr(), dA.data_ptr(), M, N, K, G,
+                                               flags, st)
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_gemm_dgrad")
+    return dA
+
+
+def gated_gemm_backward(dH, gate, up, wt_gate, S_gate, wt_up, S_up, K: int, G: int, act: int = ACT_SILU, out=None,
+                        out_gate=None, out_up=None, flags: int = 0, stream=None):
+    """Backward of gated_gemm with frozen weights: (dA [M, K], d_gate [M, N], d_up [M, N]) from the gradient dH
+    [M, N] and the projections that gated_gemm(..., save=True) returned."""
+    dH = _half_matrix("dH", dH)
+    M, N = dH.shape
+    gate, up = _half_matrix("gate", gate, dH, (M, N)), _half_matrix("up", up, dH, (M, N))
+    S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, dH)
+    S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, dH)
+    dA = _output("out", out, (M, K), dH)
+    dG, dU = _output("out_gate", out_gate, (M, N), dH), _output("out_up", out_up, (M, N), dH)
+    if M == 0:
+        return dA, dG, dU
+    with _on_device(dH):
+        st = _current_stream(dH.device.index) if stream is None else _stream(stream)
+        rc = (_lib or load()).w4a16_gated_gemm_backward(
+            dH.data_ptr(), gate.data_ptr(), up.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(), wt_up.data_ptr(),
+            S_up.data_ptr(), dG.data_ptr(), dU.data_ptr(), dA.data_ptr(), M, N, K, G, act, flags, st)
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_gated_gemm_backward")
+    return dA, dG, dU
 
 
 def device_status(clear: bool = True) -> int:

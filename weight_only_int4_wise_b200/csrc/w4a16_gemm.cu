@@ -51,6 +51,7 @@
 #include "epilogue.cuh"
 #include "ptx.cuh"
 #include "w4a16_internal.h"
+#include "waits.cuh"
 
 namespace w4a16 {
 
@@ -67,7 +68,6 @@ constexpr int kPrefetchStages = 12;        // int4 tile stages the producer pull
 // DQ-th stage, so DQ groups keep DQ stages in flight).
 __host__ __device__ constexpr int threads_for(int dq) { return (2 + kGroupWarps * dq) * 32; }
 static_assert(threads_for(4) <= 1024, "the 256-row tile's four dequantisation groups fit a CTA");
-constexpr long long kTimeoutCycles = 4000000000ll;  // about 2 s per wait at the boost clock
 
 struct Params {
     const uint8_t* wt[W4A16_MAX_EXPERTS];   // tiled weights (dense: [0])
@@ -126,68 +126,18 @@ struct Layout {
 
 __device__ __forceinline__ void latch_status(int code) { atomicCAS(&g_status, 0, code); }
 
-
-// Bounded wait on an mbarrier phase. Returns false if the CTA is aborting or
-// the wait ran out (which starts the abort). The bound is counted in SM clock
-// cycles (clock64 is a cheap, SM-local register; the global timer is far slower
-// to read and would add its latency to every pipeline hand-off).
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
-    if (mbar_try_wait(bar, parity)) return true;
-    long long start = 0;
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 15u) == 0) {
-            if (*abort_flag) return false;
-            const long long now = clock64();
-            if (start == 0) {
-                start = now;
-            } else if (now - start > limit) {
-                *abort_flag = 1;
-                latch_status(W4A16_ERR_TIMEOUT);
-                return false;
-            }
-        }
-    }
+    return wait_phase(bar, parity, abort_flag, limit, &g_status);
 }
-
-// Bounded wait that ignores the abort flag: used where in-flight asynchronous
-// work must finish before its resources are released.
 __device__ __forceinline__ bool drain_phase(uint64_t* bar, uint32_t parity) {
-    const long long limit = kTimeoutCycles;  // drains keep the long bound whatever the wait bound is
-    long long start = 0;
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 15u) == 15u) {
-            const long long now = clock64();
-            if (start == 0) {
-                start = now;
-            } else if (now - start > limit) {
-                latch_status(W4A16_ERR_TIMEOUT);
-                return false;
-            }
-        }
-    }
+    return drain_phase(bar, parity, &g_status);
 }
-
-// Warp-collective forms: lane 0 polls (so the timeout decision is the same for
-// the whole warp), then every lane observes the completed phase itself, which
-// gives each lane acquire ordering on the data the phase guards. The phase
-// cannot move on before this warp arrives elsewhere, so that check is immediate.
 __device__ __forceinline__ bool warp_wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                 long long limit) {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = wait_phase(bar, parity, abort_flag, limit) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok) mbar_try_wait(bar, parity);
-    return ok != 0;
+    return warp_wait_phase(bar, parity, abort_flag, limit, &g_status);
 }
-
 __device__ __forceinline__ bool warp_drain_phase(uint64_t* bar, uint32_t parity) {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = drain_phase(bar, parity) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok) mbar_try_wait(bar, parity);
-    return ok != 0;
+    return warp_drain_phase(bar, parity, &g_status);
 }
 
 // OG: G is a multiple of 64, so a stage lies inside one scale group.
@@ -871,12 +821,6 @@ int token_tile_for(int64_t rows_per_tile) {
     return 256;
 }
 
-int check_shape(int64_t N, int64_t K, int64_t G) {
-    if (N <= 0 || K <= 0 || G <= 0) return W4A16_ERR_INVALID_ARG;
-    if (N % 8 || K % 8 || G % 16) return W4A16_ERR_UNSUPPORTED;
-    if (N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return W4A16_ERR_UNSUPPORTED;
-    return W4A16_OK;
-}
 
 struct Plan {
     int bn;
@@ -1106,6 +1050,13 @@ int encode_activation_map(CUtensorMap* map, const void* A, int64_t rows, int64_t
     return r == CUDA_SUCCESS ? W4A16_OK : W4A16_ERR_CUDA;
 }
 
+int check_shape(int64_t N, int64_t K, int64_t G) {
+    if (N <= 0 || K <= 0 || G <= 0) return W4A16_ERR_INVALID_ARG;
+    if (N % 8 || K % 8 || G % 16) return W4A16_ERR_UNSUPPORTED;
+    if (N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+
 int activation_map(CUtensorMap* map, const void* A, int64_t rows, int64_t K, int box_rows) {
     // A small per-thread cache: the encoder costs more than the rest of a
     // decode-sized call on the host, and the same activation buffers recur.
@@ -1183,13 +1134,11 @@ std::atomic<long long> g_wait_limit{kTimeoutCycles};  // test aid: w4a16_set_fau
 std::atomic<int> g_stall_stage{-1};
 }
 
+long long device_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+int injected_stall_stage() { return g_stall_stage.load(std::memory_order_relaxed); }
+
 // Set by the entry points with per-call flags for the duration of one call on this host thread.
 thread_local int t_call_static_weights = 0;
-
-struct CallStaticWeights {
-    explicit CallStaticWeights(bool on) { t_call_static_weights = on ? 1 : 0; }
-    ~CallStaticWeights() { t_call_static_weights = 0; }
-};
 
 bool static_weights_enabled() {
     return t_call_static_weights != 0 || g_static_weights.load(std::memory_order_relaxed) != 0;
@@ -1484,8 +1433,9 @@ extern "C" int w4a16_device_status(int clear) {
     const int vs = skinny_device_status(clear != 0);
     const int vq = quant_device_status(clear != 0);
     const int vm = moe_device_status(clear != 0);
-    if (vs < 0 || vq < 0 || vm < 0) return W4A16_ERR_CUDA;
-    return v != 0 ? v : (vs != 0 ? vs : (vq != 0 ? vq : vm));
+    const int vd = dgrad_device_status(clear != 0);
+    if (vs < 0 || vq < 0 || vm < 0 || vd < 0) return W4A16_ERR_CUDA;
+    return v != 0 ? v : (vs != 0 ? vs : (vq != 0 ? vq : (vm != 0 ? vm : vd)));
 }
 
 extern "C" int w4a16_set_fault_injection(int64_t stall_stage, int64_t wait_limit_cycles) {

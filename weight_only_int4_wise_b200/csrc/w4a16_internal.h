@@ -20,6 +20,13 @@ int sm_count();
 // Whether the caller declared weights and scales static (w4a16_set_static_weights).
 bool static_weights_enabled();
 
+// W4A16_FLAG_STATIC_WEIGHTS for the duration of one call on this host thread.
+extern thread_local int t_call_static_weights;
+struct CallStaticWeights {
+    explicit CallStaticWeights(bool on) { t_call_static_weights = on ? 1 : 0; }
+    ~CallStaticWeights() { t_call_static_weights = 0; }
+};
+
 // A tiled tensor map over fp16 elements [outer, inner] (row stride in bytes),
 // box [box_outer, box_inner], no swizzle, zero fill outside the tensor.
 // W4A16_OK, or W4A16_ERR_CUDA if the driver's encoder is missing or refuses.
@@ -45,6 +52,17 @@ int moe_device_status(bool clear);
 
 // The quantiser kernel's latched device status (0 = none, -1 if it could not be read).
 int quant_device_status(bool clear);
+
+// The transposed product's latched device status (0 = none, -1 if it could not be read).
+int dgrad_device_status(bool clear);
+
+// The bound of every device wait in SM clock cycles, and the stage whose ready
+// signal is withheld (-1: none): w4a16_set_fault_injection.
+long long device_wait_limit();
+int injected_stall_stage();
+
+// Argument checks that the products share: sizes of a weight matrix, alignment.
+int check_shape(int64_t N, int64_t K, int64_t G);
 
 // Decode-sized products (M <= kSkinnyMaxM) run on the skinny kernel.
 constexpr int kSkinnyMaxM = 16;
