@@ -66,8 +66,9 @@ enum {
     W4A16_ERR_BAD_OFFSETS = 6,  /* device status: expert offsets not 0 = o[0] <= ... <= o[E] = rows */
     W4A16_ERR_BAD_ROUTING = 7,  /* device status: an expert id out of range or repeated within a token,
                                    or a gathered-row index out of range */
-    W4A16_ERR_SCRATCH_TOO_SMALL = 8  /* w4a16_moe_layer_static: the shape needs more intermediates than
+    W4A16_ERR_SCRATCH_TOO_SMALL = 8, /* w4a16_moe_layer_static: the shape needs more intermediates than
                                         the library's static scratch holds */
+    W4A16_ERR_BAD_ADAPTER = 9    /* device status: an adapter index of w4a16_lora_gemm not below L */
 };
 
 /* Elementwise activations of the expert layer (Int4 Moe Plugin page,
@@ -336,6 +337,38 @@ int w4a16_gated_gemm_backward(const w4a16_half* dH_dev, const w4a16_half* Pg_dev
                               const w4a16_half* S_up_dev, w4a16_half* dPg_dev, w4a16_half* dPu_dev,
                               w4a16_half* dA_dev, int64_t M, int64_t N, int64_t K, int64_t G, int act,
                               uint32_t flags, void* stream);
+
+/* Largest rank w4a16_lora_gemm accepts. */
+#define W4A16_MAX_RANK 128
+
+/* The shared product with one low-rank adapter per row (many requests in one
+ * batch, each with its own adapter or none):
+ *     C[m] = fp16( A[m] W + scaling[i] * (A[m] LA[i]^T) LB[i]^T ),  i = ids[m],
+ * A_dev [M, K], C_dev [M, N], W as above; LA_dev [L, R, K] and LB_dev [L, N, R]
+ * fp16, the L adapters stacked (an adapter of a lower rank is padded with zero
+ * rows of LA and zero columns of LB); scaling_dev [L] fp32 (NULL: all 1);
+ * ids_dev [M] int32 on the device, a negative index meaning no adapter. Rows of
+ * one adapter need not be neighbours. An index not below L latches
+ * W4A16_ERR_BAD_ADAPTER and its row is computed without an adapter.
+ * Sums are fp32 and C is rounded once. V = scaling * A LA^T must stay within
+ * fp16's range: for M > 16 it is rounded to fp16 before its product with LB (a
+ * further 2^-12 of the adapter's part, like the weights' own rounding). For M <=
+ * 16 the shared part is scaled as w4a16_gemm does it. A row's values never
+ * reach another row's output, and neither does an infinity or NaN in the LB of an
+ * adapter that the row does not use.
+ * R a multiple of 8 up to W4A16_MAX_RANK, 1 <= L < 2^31. workspace_dev:
+ * w4a16_lora_workspace_size(M, R) bytes, caller-owned, not initialised; calls
+ * that may overlap on the GPU must not share it. A, Wt, S, LA, LB and the
+ * workspace 16-byte aligned, ids and scaling 4-byte, C 2-byte; contract of
+ * w4a16_gemm otherwise. M == 0 is a no-op. Errors: INVALID_ARG (also a workspace
+ * that is too small), MISALIGNED, UNSUPPORTED, CUDA. */
+int w4a16_lora_gemm(const w4a16_half* A_dev, const uint8_t* Wt_dev, const w4a16_half* S_dev,
+                    const w4a16_half* LA_dev, const w4a16_half* LB_dev, const int32_t* ids_dev,
+                    const float* scaling_dev, w4a16_half* C_dev, int64_t M, int64_t N, int64_t K, int64_t G,
+                    int64_t L, int64_t R, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace w4a16_lora_gemm needs; -1 for invalid sizes. */
+int64_t w4a16_lora_workspace_size(int64_t M, int64_t R);
 
 /* Declares (enable != 0) or withdraws (enable == 0) the promise that no
  * kernel on the calling streams writes the tiled weights or the scales passed

@@ -14,8 +14,9 @@ from ._lib import (  # noqa: F401
     w8a16_gemm, w8a16_gemm_launch_info, repack_w8, gemm_w8, w4a16_moe_layer_static, w4a16_moe_static_scratch_bytes,
     w4a16_gemm_ex, FLAG_STATIC_WEIGHTS, w8a16_quantize, quantize_w8,
     w4a16_gated_gemm, gated_gemm, w4a16_gemm_dgrad, gemm_dgrad, w4a16_gated_gemm_backward, gated_gemm_backward,
+    w4a16_lora_gemm, w4a16_lora_workspace_size, lora_gemm, MAX_RANK,
 )
 from ._lib import (  # noqa: F401
-    ACT_GELU_ERF, ACT_GELU_TANH, ACT_IDENTITY, ACT_RELU, ACT_SILU, ERR_BAD_OFFSETS, ERR_BAD_ROUTING, ERR_CUDA,
+    ACT_GELU_ERF, ACT_GELU_TANH, ACT_IDENTITY, ACT_RELU, ACT_SILU, ERR_BAD_ADAPTER, ERR_BAD_OFFSETS, ERR_BAD_ROUTING, ERR_CUDA,
     ERR_INVALID_ARG, ERR_MISALIGNED, ERR_SCRATCH_TOO_SMALL, ERR_TIMEOUT, ERR_UNSUPPORTED, OK,
 )

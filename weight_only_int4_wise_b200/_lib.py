@@ -25,8 +25,10 @@ ERR_TIMEOUT = 5
 ERR_BAD_OFFSETS = 6
 ERR_BAD_ROUTING = 7
 ERR_SCRATCH_TOO_SMALL = 8
+ERR_BAD_ADAPTER = 9
 MAX_EXPERTS = 64
 MAX_TOPK = 8
+MAX_RANK = 128
 FLAG_STATIC_WEIGHTS = 1
 ACT_IDENTITY = 0
 ACT_RELU = 1
@@ -44,6 +46,7 @@ EXPORTED = [
     "w8a16_tiled_bytes", "w8a16_repack", "w8a16_gemm", "w8a16_gemm_launch_info",
     "w4a16_moe_layer_static", "w4a16_moe_static_scratch_bytes", "w4a16_gemm_ex", "w8a16_quantize",
     "w4a16_gated_gemm", "w4a16_gemm_dgrad", "w4a16_gated_gemm_backward",
+    "w4a16_lora_gemm", "w4a16_lora_workspace_size",
 ]
 
 
@@ -156,6 +159,10 @@ def load() -> ctypes.CDLL:
         lib.w4a16_gemm_dgrad.restype = ctypes.c_int
         lib.w4a16_gated_gemm_backward.argtypes = [_vp] * 10 + [_i64] * 4 + [ctypes.c_int, ctypes.c_uint32, _vp]
         lib.w4a16_gated_gemm_backward.restype = ctypes.c_int
+        lib.w4a16_lora_gemm.argtypes = [_vp] * 8 + [_i64] * 6 + [_vp, _i64, _vp]
+        lib.w4a16_lora_gemm.restype = ctypes.c_int
+        lib.w4a16_lora_workspace_size.argtypes = [_i64, _i64]
+        lib.w4a16_lora_workspace_size.restype = _i64
         _lib = lib
     return _lib
 
@@ -372,6 +379,16 @@ def w4a16_gated_gemm_backward(dH, Pg, Pu, Wt_gate, S_gate, Wt_up, S_up, dPg, dPu
                                             G, act, flags, _stream(stream))
 
 
+def w4a16_lora_workspace_size(M: int, R: int) -> int:
+    return int(load().w4a16_lora_workspace_size(M, R))
+
+
+def w4a16_lora_gemm(A, Wt, S, LA, LB, ids, scaling, C, M: int, N: int, K: int, G: int, L: int, R: int, workspace,
+                    workspace_bytes: int, stream=None) -> int:
+    return load().w4a16_lora_gemm(_addr(A), _addr(Wt), _addr(S), _addr(LA), _addr(LB), _addr(ids), _addr(scaling),
+                                  _addr(C), M, N, K, G, L, R, _addr(workspace), workspace_bytes, _stream(stream))
+
+
 def w4a16_gemm_launch_info(M: int, N: int, K: int, G: int):
     info = LaunchInfo()
     rc = load().w4a16_gemm_launch_info(M, N, K, G, ctypes.byref(info))
@@ -541,55 +558,78 @@ def gemm_w8(A, wt8, S, N: int, G: int, out=None, stream=None):
     return C
 
 
-def _half_matrix(name: str, t, like=None, shape=None):
-    """A CUDA fp16 matrix operand, dense (a copy if it is not); `like`: the tensor whose device it must share."""
-    import torch
-    if not t.is_cuda or (like is not None and t.device != like.device):
-        raise ValueError(f"{name} must live on the same CUDA device as the other operands")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be float16")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be a matrix" + ("" if shape is None else f" of shape {list(shape)}")
-                         + f", got {list(t.shape)}")
+def _operand(name: str, t, dtype, shape, like):
+    """A dense CUDA operand of a given type and shape on `like`'s device (a dense copy if it is strided)."""
+    if t.device != like.device:
+        raise ValueError(f"{name} must live on {like.device}, as the other operands do")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _weight_operand(name: str, wt, S, K: int, N: int, G: int, like):
-    """Tiled int4 weights [K, N] and their scales, checked for size; returns the dense scales."""
+def _rows_operand(name: str, t):
+    """The CUDA fp16 matrix that a call's rows come from; sets the call's device."""
     import torch
-    if wt.device != like.device:
-        raise ValueError(f"{name} must live on the same CUDA device as the other operands")
+    if not t.is_cuda:
+        raise ValueError("all tensors must live on a CUDA device")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {list(t.shape)}")
+    return t
+
+
+def _weight_operand(name: str, wt, S, K: int, N: int, G: int, like):
+    """Checks tiled int4 weights [K, N] against their sizes; returns the dense scales."""
+    import torch
     if G <= 0:
         raise W4A16Error(ERR_INVALID_ARG, name)
-    if wt.dtype != torch.uint8 or wt.numel() != ((K + 63) // 64) * ((N + 127) // 128) * 4096 or not wt.is_contiguous():
-        raise ValueError(f"{name} must be the tiled layout of [{K}, {N}] codes (flat uint8)")
-    return _half_matrix(f"the scales of {name}", S, like, ((K + G - 1) // G, N))
+    if (wt.device != like.device or wt.dtype != torch.uint8 or not wt.is_contiguous()
+            or wt.numel() != ((K + 63) // 64) * ((N + 127) // 128) * 4096):
+        raise ValueError(f"{name} must be the tiled layout of [{K}, {N}] codes (dense uint8) on {like.device}")
+    return _operand(f"the scales of {name}", S, torch.float16, ((K + G - 1) // G, N), like)
 
 
 def _output(name: str, out, shape, like):
     import torch
     if out is None:
         return torch.empty(shape, dtype=torch.float16, device=like.device)
-    if out.device != like.device or out.dtype != torch.float16 or tuple(out.shape) != shape or not out.is_contiguous():
+    if out.device != like.device or out.dtype != torch.float16 or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"{name} must be a dense float16 tensor of shape {list(shape)} on {like.device}")
     return out
 
 
-class _on_device:
-    """Makes a tensor's device current for one call, if it is not already."""
+class _launch_on:
+    """The device of `tensor` and, if one is given, `stream` (a torch stream or a raw handle) made current for one
+    call, so that the copies and buffers that the call makes belong to the stream its kernels run on. Yields the
+    stream's raw handle."""
 
-    def __init__(self, tensor):
-        import torch
-        index = tensor.device.index
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    __slots__ = ("index", "stream", "guards")
+
+    def __init__(self, tensor, stream):
+        self.index, self.stream, self.guards = tensor.device.index, stream, ()
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        import torch
+        if self.stream is None and self.index == torch.cuda.current_device():
+            return _current_stream(self.index)
+        self.guards = [torch.cuda.device(self.index)]
+        self.guards[0].__enter__()
+        if self.stream is not None:
+            raw = _stream(self.stream)
+            st = self.stream if isinstance(self.stream, torch.cuda.Stream) else (
+                torch.cuda.ExternalStream(raw, device=self.index) if raw else torch.cuda.default_stream(self.index))
+            self.guards.append(torch.cuda.stream(st))
+            self.guards[1].__enter__()
+            return raw
+        return _current_stream(self.index)
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        for guard in reversed(self.guards):
+            guard.__exit__(*exc)
+        return False
 
 
 def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_SILU, save: bool = False, out=None,
@@ -597,41 +637,37 @@ def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_S
     """H [M, N] fp16 = act(A x W_gate) * (A x W_up) from activations A [M, K] fp16 and two tiled weight
     matrices [K, N] with scales [ceil(K/G), N]; one rounding. With save=True returns (H, gate, up), the two
     projections in fp16 as gated_gemm_backward reads them."""
-    A = _half_matrix("A", A)
-    M, K = A.shape
-    S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, A)
-    S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, A)
-    H = _output("out", out, (M, N), A)
-    Pg = Pu = None
-    if save:
-        Pg, Pu = _output("out_gate", out_gate, (M, N), A), _output("out_up", out_up, (M, N), A)
-    if M == 0:  # (an empty tensor has no address to pass)
-        return (H, Pg, Pu) if save else H
-    with _on_device(A):
-        st = _current_stream(A.device.index) if stream is None else _stream(stream)
-        rc = (_lib or load()).w4a16_gated_gemm(A.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(), wt_up.data_ptr(),
-                                               S_up.data_ptr(), H.data_ptr(), _addr(Pg), _addr(Pu), M, N, K, G, act,
-                                               flags, st)
-    if rc != OK:
-        raise W4A16Error(rc, "w4a16_gated_gemm")
+    M, K = _rows_operand("A", A).shape
+    with _launch_on(A, stream) as st:
+        A = A if A.is_contiguous() else A.contiguous()
+        S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, A)
+        S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, A)
+        H = _output("out", out, (M, N), A)
+        Pg = _output("out_gate", out_gate, (M, N), A) if save else None
+        Pu = _output("out_up", out_up, (M, N), A) if save else None
+        if M:  # (an empty tensor has no address to pass)
+            rc = (_lib or load()).w4a16_gated_gemm(A.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(),
+                                                   wt_up.data_ptr(), S_up.data_ptr(), H.data_ptr(),
+                                                   Pg.data_ptr() if save else None, Pu.data_ptr() if save else None,
+                                                   M, N, K, G, act, flags, st)
+            if rc != OK:
+                raise W4A16Error(rc, "w4a16_gated_gemm")
     return (H, Pg, Pu) if save else H
 
 
 def gemm_dgrad(dC, wt, S, K: int, G: int, out=None, flags: int = 0, stream=None):
     """dA [M, K] fp16 = dC [M, N] x W^T, the gradient of gemm's input, from the forward product's tiled weights
     and scales [ceil(K/G), N]."""
-    dC = _half_matrix("dC", dC)
-    M, N = dC.shape
-    S = _weight_operand("wt", wt, S, K, N, G, dC)
-    dA = _output("out", out, (M, K), dC)
-    if M == 0:
-        return dA
-    with _on_device(dC):
-        st = _current_stream(dC.device.index) if stream is None else _stream(stream)
-        rc = (_lib or load()).w4a16_gemm_dgrad(dC.data_ptr(), wt.data_ptr(), S.data_ptr(), dA.data_ptr(), M, N, K, G,
-                                               flags, st)
-    if rc != OK:
-        raise W4A16Error(rc, "w4a16_gemm_dgrad")
+    M, N = _rows_operand("dC", dC).shape
+    with _launch_on(dC, stream) as st:
+        dC = dC if dC.is_contiguous() else dC.contiguous()
+        S = _weight_operand("wt", wt, S, K, N, G, dC)
+        dA = _output("out", out, (M, K), dC)
+        if M:
+            rc = (_lib or load()).w4a16_gemm_dgrad(dC.data_ptr(), wt.data_ptr(), S.data_ptr(), dA.data_ptr(), M, N,
+                                                   K, G, flags, st)
+            if rc != OK:
+                raise W4A16Error(rc, "w4a16_gemm_dgrad")
     return dA
 
 
@@ -639,23 +675,59 @@ def gated_gemm_backward(dH, gate, up, wt_gate, S_gate, wt_up, S_up, K: int, G: i
                         out_gate=None, out_up=None, flags: int = 0, stream=None):
     """Backward of gated_gemm with frozen weights: (dA [M, K], d_gate [M, N], d_up [M, N]) from the gradient dH
     [M, N] and the projections that gated_gemm(..., save=True) returned."""
-    dH = _half_matrix("dH", dH)
-    M, N = dH.shape
-    gate, up = _half_matrix("gate", gate, dH, (M, N)), _half_matrix("up", up, dH, (M, N))
-    S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, dH)
-    S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, dH)
-    dA = _output("out", out, (M, K), dH)
-    dG, dU = _output("out_gate", out_gate, (M, N), dH), _output("out_up", out_up, (M, N), dH)
-    if M == 0:
-        return dA, dG, dU
-    with _on_device(dH):
-        st = _current_stream(dH.device.index) if stream is None else _stream(stream)
-        rc = (_lib or load()).w4a16_gated_gemm_backward(
-            dH.data_ptr(), gate.data_ptr(), up.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(), wt_up.data_ptr(),
-            S_up.data_ptr(), dG.data_ptr(), dU.data_ptr(), dA.data_ptr(), M, N, K, G, act, flags, st)
-    if rc != OK:
-        raise W4A16Error(rc, "w4a16_gated_gemm_backward")
+    import torch
+    M, N = _rows_operand("dH", dH).shape
+    with _launch_on(dH, stream) as st:
+        dH = dH if dH.is_contiguous() else dH.contiguous()
+        gate = _operand("gate", gate, torch.float16, (M, N), dH)
+        up = _operand("up", up, torch.float16, (M, N), dH)
+        S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, dH)
+        S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, dH)
+        dA = _output("out", out, (M, K), dH)
+        dG, dU = _output("out_gate", out_gate, (M, N), dH), _output("out_up", out_up, (M, N), dH)
+        if M:
+            rc = (_lib or load()).w4a16_gated_gemm_backward(
+                dH.data_ptr(), gate.data_ptr(), up.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(),
+                wt_up.data_ptr(), S_up.data_ptr(), dG.data_ptr(), dU.data_ptr(), dA.data_ptr(), M, N, K, G, act,
+                flags, st)
+            if rc != OK:
+                raise W4A16Error(rc, "w4a16_gated_gemm_backward")
     return dA, dG, dU
+
+
+def lora_gemm(A, wt, S, N: int, G: int, lora_A, lora_B, ids, scaling=None, workspace=None, out=None, stream=None):
+    """C [M, N] fp16 = A x W + scaling[i] * (A x lora_A[i]^T) x lora_B[i]^T with i = ids[m] for each row m (negative:
+    no adapter): one shared 4-bit projection and stacked adapters lora_A [L, R, K], lora_B [L, N, R] fp16, ids [M]
+    int32 and scaling [L] float32 (None: 1) on the device. The workspace (uint8, w4a16_lora_workspace_size(M, R)
+    bytes) is allocated here when not given."""
+    import torch
+    M, K = _rows_operand("A", A).shape
+    if lora_A.dim() != 3:
+        raise ValueError(f"lora_A must be [L, R, K], got {list(lora_A.shape)}")
+    L, R = lora_A.shape[0], lora_A.shape[1]
+    with _launch_on(A, stream) as st:
+        A = A if A.is_contiguous() else A.contiguous()
+        S = _weight_operand("wt", wt, S, K, N, G, A)
+        lora_A = _operand("lora_A", lora_A, torch.float16, (L, R, K), A)
+        lora_B = _operand("lora_B", lora_B, torch.float16, (L, N, R), A)
+        ids = _operand("ids", ids, torch.int32, (M,), A)
+        if scaling is not None:
+            scaling = _operand("scaling", scaling, torch.float32, (L,), A)
+        C = _output("out", out, (M, N), A)
+        if M:
+            lib = _lib or load()
+            need = lib.w4a16_lora_workspace_size(M, R)
+            if workspace is None:
+                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=A.device)
+            elif workspace.device != A.device or not workspace.is_contiguous():
+                raise ValueError(f"the workspace must be a dense tensor on {A.device}")
+            rc = lib.w4a16_lora_gemm(A.data_ptr(), wt.data_ptr(), S.data_ptr(), lora_A.data_ptr(), lora_B.data_ptr(),
+                                     ids.data_ptr(), None if scaling is None else scaling.data_ptr(), C.data_ptr(),
+                                     M, N, K, G, L, R, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), st)
+            if rc != OK:
+                raise W4A16Error(rc, "w4a16_lora_gemm")
+    return C
 
 
 def device_status(clear: bool = True) -> int:

@@ -90,6 +90,7 @@ struct Params {
     // is H, and Pg / Pu (both or neither) take the projections themselves.
     __half* Pg;
     __half* Pu;
+    LoraOperands lora;  // adapter form
 };
 
 // What a launch computes. kPlain: the dense or the grouped-expert product.
@@ -97,7 +98,13 @@ struct Params {
 // 0..63 hold their gate columns and lanes 64..127 the same up columns, so one
 // MMA sequence over one activation stream makes both projections, at the cost
 // of a dense product twice as wide; the epilogue pairs the two halves.
-enum GemmForm { kPlain = 0, kGated = 1 };
+// kLora: the dense product plus V[m] LB[ids[m]]^T. The distinct adapters of the
+// CTA's token tile form further contraction stages behind those of K, 64 values
+// of (adapter, rank) each: the dequantising warps put LB's rows in the weights'
+// TMEM slot and, in the activations' slot, V's rows rounded to fp16 where the row
+// uses that adapter and zeros elsewhere. So the adapters join the same fp32
+// accumulator and cost D * R / 64 more stages for D adapters in the tile.
+enum GemmForm { kPlain = 0, kGated = 1, kLora = 2 };
 
 // One ring of LS stages. Stage s owns, in shared memory, an activation tile
 // and, in tensor memory, a 32-column slot for the dequantised fp16 weights;
@@ -140,6 +147,20 @@ __device__ __forceinline__ bool warp_drain_phase(uint64_t* bar, uint32_t parity)
     return warp_drain_phase(bar, parity, &g_status);
 }
 
+// Adapter form: the index of the first adapter stage (the ring is taken by whole
+// pairs of stages) and the number of adapter stages, which the first CTA of a
+// K split takes; V and the tile's list come from the kernel before this one.
+__device__ __forceinline__ int lora_first(int nst) { return (nst + 1) & ~1; }
+__device__ __forceinline__ int lora_stages(const Params& p, int split) {
+    grid_dependency_wait();
+    return split == 0 ? (__ldcg(p.lora.count + blockIdx.z) * (p.lora.R / 8) + 7) / 8 : 0;
+}
+
+// 0xFFFF in each half of x that holds an infinity or NaN (its exponent field is all ones).
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t x) {
+    return ((((x & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u) * 0xFFFFu;
+}
+
 // OG: G is a multiple of 64, so a stage lies inside one scale group.
 // BITS: 4 for the int4 tiled layout, 8 for the 8-bit code layout (W8A16): a
 // stage's tile is 4 or 8 KB, and a thread loads 2 or 4 16-byte chunks of its
@@ -149,8 +170,8 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
     w4a16_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ Params p) {
     using L = Layout<BN, LS, TMEM_COLS>;
     static_assert(BITS == 4 || BITS == 8, "int4 or 8-bit codes");
-    constexpr bool GATED = FORM == kGated;
-    static_assert(!GATED || BITS == 4, "the gated form reads int4 codes");
+    constexpr bool GATED = FORM == kGated, LORA = FORM == kLora;
+    static_assert(FORM == kPlain || BITS == 4, "the gated and adapter forms read int4 codes");
     constexpr int kCols = GATED ? kTileN / 2 : kTileN;  // output columns of a CTA
     constexpr int kTileBytes = BITS == 4 ? kRawBytes : 2 * kRawBytes;  // one 128 x 64 tile of codes
     constexpr int kChunks = BITS / 2;                                  // 16-byte chunks per column and stage
@@ -165,7 +186,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
     uint64_t* accfull = done + LS;                                   // accumulator complete
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-    int* tile_info = reinterpret_cast<int*>(smem + L::kMisc + 8);  // has_tile, expert, m0, rows, staged
+    int* tile_info = reinterpret_cast<int*>(smem + L::kMisc + 8);  // has_tile, expert, m0, rows, staged, bad LB
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -250,6 +271,10 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
     const uint8_t* wcol =
         p.wt[GATED ? half : expert] + static_cast<int64_t>(wtile_n) * p.KT * kTileBytes + wtile_j * 16;
     const __half* scol = p.sc[GATED ? half : expert] + (col_ok ? n : 0);
+    // (Adapter form: weights, scales and activations are read past L1 without waiting
+    // for the kernel that makes V, which lets this one start only once everything
+    // before it is complete; see the wait before the adapter stages.)
+    auto load_scale = [](const __half* q) { return LORA ? __ldcg(q) : __ldg(q); };
     int li = grp;
     int kk = (kb + grp) * kTileK;
     int gk = kk / p.G;
@@ -257,9 +282,10 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         if (li < nst) {
             const uint8_t* src = wcol + static_cast<int64_t>(kb + li) * kTileBytes;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) r[c] = ld_nc_v4(src + c * 2048);
+            for (int c = 0; c < kChunks; ++c)
+                r[c] = LORA ? __ldcg(reinterpret_cast<const uint4*>(src + c * 2048)) : ld_nc_v4(src + c * 2048);
             if constexpr (OG) {
-                sv[0] = __ldg(scol + static_cast<int64_t>(min(gk, p.ngroups - 1)) * p.N);
+                sv[0] = load_scale(scol + static_cast<int64_t>(min(gk, p.ngroups - 1)) * p.N);
             } else {
                 const int rem = kk - gk * p.G;
 #pragma unroll
@@ -269,7 +295,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
                         r2 -= p.G;
                         ++g;
                     }
-                    sv[q] = __ldg(scol + static_cast<int64_t>(min(g, p.ngroups - 1)) * p.N);
+                    sv[q] = load_scale(scol + static_cast<int64_t>(min(g, p.ngroups - 1)) * p.N);
                 }
             }
         } else {
@@ -285,7 +311,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
     uint4 rq0[kChunks], rq1[kChunks];
     __half sq0[kScales], sq1[kScales];
     if (warp >= 2) {
-        if (!p.prefetch) grid_dependency_wait();  // weights and scales may come from the previous kernel
+        if (!LORA && !p.prefetch) grid_dependency_wait();  // weights and scales may come from the previous kernel
         load_next(rq0, sq0);
         load_next(rq1, sq1);
     }
@@ -298,6 +324,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         for (int q = 0; q < LS / 2; ++q) mbar_init(&afull[q], 2 * kGroupWarps);
         mbar_init(accfull, 1);
         *abort_flag = 0;
+        tile_info[5] = 0;
         fence_mbar_init();
         prefetch_tensor_map(&tmA);
         grid_launch_dependents();
@@ -317,7 +344,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         // A stage's slot is free again once the MMAs that read it completed
         // (which also means the dequantisation warps finished reading it).
         if (lane == 0) {
-            grid_dependency_wait();  // the activations may be written by the previous kernel
+            if (!LORA) grid_dependency_wait();  // the activations may be written by the previous kernel
             // The int4 tile of a stage is one contiguous 4 KB block: pull it into
             // L2 kPrefetchStages ahead, so that the dequantising threads' own
             // loads (issued only kAhead of their stages ahead) find it there.
@@ -378,8 +405,28 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
                             mma_f16_ts(tmem_acc, a0 + 16, bdesc + 4, idesc, 1u);
                             mma_f16_ts(tmem_acc, a0 + 24, bdesc + 6, idesc, 1u);
                             mma_commit(&done[s]);
+                        } else if (LORA) {
+                            mma_commit(&done[2 * qq + t]);  // the skipped partner of an odd last stage
                         }
                     }
+                }
+            }
+            if constexpr (LORA) {
+                // The adapter stages, in the same ring from the next whole pair on.
+                const int first = lora_first(nst), end = first + lora_stages(p, split);
+                for (int i = first; i < end && !stop; ++i) {
+                    const int s = i % LS;
+                    if ((i & 1) == 0 &&
+                        !wait_phase(&afull[s >> 1], static_cast<uint32_t>(i / LS) & 1u, abort_flag, p.wait_limit))
+                        break;
+                    tc_fence_after_sync();
+                    const uint64_t bdesc = smem_desc_k_sw128(smem_addr(smem + L::kAct + s * L::kActBytes));
+                    const uint32_t a0 = tmem_ring + static_cast<uint32_t>(s * kSlotCols);
+                    mma_f16_ts(tmem_acc, a0, bdesc, idesc, 1u);
+                    mma_f16_ts(tmem_acc, a0 + 8, bdesc + 2, idesc, 1u);
+                    mma_f16_ts(tmem_acc, a0 + 16, bdesc + 4, idesc, 1u);
+                    mma_f16_ts(tmem_acc, a0 + 24, bdesc + 6, idesc, 1u);
+                    mma_commit(&done[s]);
                 }
             }
             mma_commit(accfull);  // fires once every MMA issued above has completed
@@ -446,6 +493,70 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
             if (i + DQ < nst && !stage(i + DQ, rq1, sq1)) break;
         }
 
+        if constexpr (LORA) {
+            const int first = lora_first(nst), end = first + lora_stages(p, split);
+            const int tid = static_cast<int>(threadIdx.x - 64) & (kGroupWarps * 32 - 1);  // inside the group
+            const int32_t* list = p.lora.list + static_cast<int64_t>(blockIdx.z) * BN;
+            const int used = end > first ? __ldcg(p.lora.count + blockIdx.z) : 0;
+            const int per = p.lora.R / 8;  // 8-rank chunks of one adapter
+            int i = first + ((grp - first) % DQ + DQ) % DQ;
+            for (; i < end; i += DQ) {
+                const int s = i % LS;
+                const int q0 = (i - first) * 8;  // chunk q of the stage: ranks 8 ((q0 + q) % per) of adapter (q0 + q) / per
+                uint32_t v[2][16];
+                uint32_t bad = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int d = (q0 + q) / per, rr = (q0 + q) - d * per;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (d < used && col_ok)
+                        x = __ldcg(reinterpret_cast<const uint4*>(
+                            p.lora.LB + (static_cast<int64_t>(__ldcg(list + d)) * p.N + n) * p.lora.R + 8 * rr));
+                    // An infinity or NaN would meet the zeros of rows that do not use
+                    // this adapter: it is left out here, and its own rows get it in
+                    // the epilogue.
+                    uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t m = nonfinite_halves(xs[e]);
+                        bad |= m;
+                        v[q >> 2][4 * (q & 3) + e] = xs[e] & ~m;
+                    }
+                }
+                if (bad) tile_info[5] = 1;
+                if (i >= LS &&
+                    !warp_wait_phase(&done[s], static_cast<uint32_t>((i / LS) - 1) & 1u, abort_flag, p.wait_limit))
+                    break;
+                tc_fence_after_sync();
+                tmem_st_32x32b_x16(tmem_ring + tlane + s * kSlotCols, v[0]);
+                tmem_st_32x32b_x16(tmem_ring + tlane + s * kSlotCols + 16, v[1]);
+                for (int row = tid; row < BN; row += kGroupWarps * 32) {
+                    const int id = row < rows ? __ldcg(p.lora.ids + m0 + row) : -1;
+                    const uint32_t dst = smem_addr(smem + L::kAct + s * L::kActBytes) + row * 128;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int d = (q0 + q) / per, rr = (q0 + q) - d * per;
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (d < used && id >= 0 && __ldcg(list + d) == id) {
+                            const float4* src =
+                                reinterpret_cast<const float4*>(p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R + 8 * rr);
+                            const float4 a = __ldcg(src), b = __ldcg(src + 1);
+                            x.x = h2_bits(__floats2half2_rn(a.x, a.y));
+                            x.y = h2_bits(__floats2half2_rn(a.z, a.w));
+                            x.z = h2_bits(__floats2half2_rn(b.x, b.y));
+                            x.w = h2_bits(__floats2half2_rn(b.z, b.w));
+                        }
+                        sts128(dst + ((q ^ (row & 7)) << 4), x);
+                    }
+                }
+                fence_proxy_async_smem();
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cnt(&afull[s >> 1], ((i & 1) == 0 && i + 1 == end) ? 2u : 1u);
+            }
+        }
+
         // -------------------------------------------------- epilogue
         // The accumulator is complete (or the CTA is aborting) once accfull fires;
         // either way no MMA may still run when TMEM is released.
@@ -454,6 +565,24 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         grid_dependency_wait();  // the output may still be read by the previous kernel
         const int aborted = __shfl_sync(0xffffffffu, *abort_flag, 0);
         bool have_acc = drained && !aborted && nst > 0;
+        // Adapter form, an LB with infinities or NaN: each output adds its own
+        // adapter's terms that the MMA left out.
+        const bool fix = LORA && have_acc && *(volatile int*)&tile_info[5] != 0;
+        auto lora_fix = [&](uint32_t (&v)[16], int c) {
+            for (int t = 0; t < 16; ++t) {
+                const int row = c * 16 + t;
+                const int id = row < rows && col_ok ? __ldcg(p.lora.ids + m0 + row) : -1;
+                if (id < 0 || id >= p.lora.L) continue;
+                const __half* b = p.lora.LB + (static_cast<int64_t>(id) * p.N + n) * p.lora.R;
+                float acc = 0.f;
+                for (int rr = 0; rr < p.lora.R; ++rr) {
+                    const float x = __half2float(__ldcg(b + rr));
+                    if (!isfinite(x))
+                        acc += __half2float(__float2half_rn(__ldcg(p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R + rr))) * x;
+                }
+                v[t] = __float_as_uint(__uint_as_float(v[t]) + acc);
+            }
+        };
         if constexpr (GATED) {
             // The epilogue's barriers need one answer for every warp: the tile is
             // written only if each of them found it complete.
@@ -519,7 +648,11 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
                     tmem_ld_32x32b_x16(tmem_acc + tlane + c * 16, v);
                     if (two) tmem_ld_32x32b_x16(tmem_acc + tlane + (c + DQ) * 16, w);
                     tmem_ld_wait();
-                    const int act = p.act;
+                    if (LORA && fix) {
+                        lora_fix(v, c);
+                        if (two) lora_fix(w, c + DQ);
+                    }
+                    const int act = LORA ? static_cast<int>(W4A16_ACT_IDENTITY) : p.act;
                     if (act == W4A16_ACT_IDENTITY) {
 #pragma unroll
                         for (int t = 0; t < 16; ++t)
@@ -546,6 +679,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
                 if (have_acc && c * 16 < n_mma) {
                     tmem_ld_32x32b_x16(tmem_acc + tlane + c * 16, v);
                     tmem_ld_wait();
+                    if (LORA && fix) lora_fix(v, c);
                 } else {
 #pragma unroll
                     for (int t = 0; t < 16; ++t) v[t] = 0u;
@@ -679,7 +813,7 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-enum Kind { kInt4 = 0, kInt8 = 1, kGatedInt4 = 2, kKinds = 3 };
+enum Kind { kInt4 = 0, kInt8 = 1, kGatedInt4 = 2, kLoraInt4 = 3, kKinds = 4 };
 
 struct Variant {
     int bn;
@@ -688,7 +822,7 @@ struct Variant {
     int tmem_cols;       // TMEM columns each resident CTA allocates
     int smem;
     // [2 * kind + (any G)]: the product with int4 codes (kind 0) and 8-bit codes (1)
-    // and the gated form (2), with G a multiple of 64 (one scale per stage) or any G
+    // and the gated (2) and adapter (3) forms, with G a multiple of 64 (one scale per stage) or any G
     const void* fn[2 * kKinds];
     int (*launch[2 * kKinds])(const CUtensorMap&, const Params&, dim3, int, int, cudaStream_t);
 };
@@ -730,13 +864,17 @@ Variant make_variant() {
                     reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 8, kPlain>),
                     reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 8, kPlain>),
                     reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 4, kGated>),
-                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 4, kGated>)},
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 4, kGated>),
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, true, 4, kLora>),
+                    reinterpret_cast<const void*>(&w4a16_gemm_kernel<BN, LS, TC, MINB, DQ, false, 4, kLora>)},
                    {&launch_variant<BN, LS, TC, MINB, DQ, true, 4, kPlain>,
                     &launch_variant<BN, LS, TC, MINB, DQ, false, 4, kPlain>,
                     &launch_variant<BN, LS, TC, MINB, DQ, true, 8, kPlain>,
                     &launch_variant<BN, LS, TC, MINB, DQ, false, 8, kPlain>,
                     &launch_variant<BN, LS, TC, MINB, DQ, true, 4, kGated>,
-                    &launch_variant<BN, LS, TC, MINB, DQ, false, 4, kGated>}};
+                    &launch_variant<BN, LS, TC, MINB, DQ, false, 4, kGated>,
+                    &launch_variant<BN, LS, TC, MINB, DQ, true, 4, kLora>,
+                    &launch_variant<BN, LS, TC, MINB, DQ, false, 4, kLora>}};
 }
 
 // Token tiles and their pipeline depths: small tiles keep two CTAs per SM; the
@@ -1170,6 +1308,7 @@ extern "C" const char* w4a16_status_string(int status) {
         case W4A16_ERR_BAD_OFFSETS: return "malformed expert offsets";
         case W4A16_ERR_BAD_ROUTING: return "expert id or gathered-row index out of range";
         case W4A16_ERR_SCRATCH_TOO_SMALL: return "shape needs more than the static scratch of the no-allocation entry point";
+        case W4A16_ERR_BAD_ADAPTER: return "adapter index out of range";
         default: return "unknown status";
     }
 }
@@ -1337,6 +1476,51 @@ int grouped_gemm_act(const w4a16_half* A_dev, const uint8_t* const* Wt, const w4
 }  // namespace w4a16
 
 namespace w4a16 {
+
+int lora_plan(int64_t M, int64_t N, int64_t K, int64_t G, LoraPlan* plan) {
+    plan->tile_rows = 0;
+    plan->skinny = skinny_plan(M, N, K, G, &plan->sk) == W4A16_OK;
+    if (plan->skinny) return W4A16_OK;
+    Plan tc;
+    const int rc = plan_dense(M, N, K, &tc, true, 0, 0, kLoraInt4);
+    if (rc) return rc;
+    plan->tile_rows = tc.bn;
+    plan->splits = tc.splits;
+    plan->grid_y = static_cast<int>(tc.grid.y);
+    plan->grid_z = static_cast<int>(tc.grid.z);
+    return W4A16_OK;
+}
+
+int lora_product(const LoraPlan& plan, const LoraOperands& lora, const w4a16_half* A, const uint8_t* Wt,
+                 const w4a16_half* S, w4a16_half* C, int64_t M, int64_t N, int64_t K, int64_t G,
+                 cudaStream_t stream) {
+    if (plan.skinny) return skinny_lora_launch(plan.sk, lora, A, Wt, S, C, M, N, K, G, stream);
+    Params p;
+    std::memset(&p, 0, sizeof(p));
+    p.wt[0] = Wt;
+    p.sc[0] = reinterpret_cast<const __half*>(S);
+    p.C = reinterpret_cast<__half*>(C);
+    p.rows = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.G = static_cast<int32_t>(G);
+    p.ngroups = static_cast<int32_t>((K + G - 1) / G);
+    p.KT = static_cast<int32_t>((K + kTileK - 1) / kTileK);
+    p.E = 1;
+    p.splits = plan.splits;
+    p.vec_out = aligned16(C);
+    p.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+    p.stall_stage = g_stall_stage.load(std::memory_order_relaxed);
+    p.lora = lora;
+    CUtensorMap map;
+    const int rc = encode_activation_map(&map, A, M, K, plan.tile_rows);
+    if (rc) return rc;
+    const Variant& v = variant_for(plan.tile_rows);
+    const dim3 grid(static_cast<unsigned>(plan.splits), static_cast<unsigned>(plan.grid_y),
+                    static_cast<unsigned>(plan.grid_z));
+    return v.launch[2 * kLoraInt4 + ((G % kTileK) ? 1 : 0)](map, p, grid, plan.splits, v.smem, stream);
+}
+
 namespace {
 
 int gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate, const w4a16_half* S_gate, const uint8_t* Wt_up,
@@ -1434,8 +1618,11 @@ extern "C" int w4a16_device_status(int clear) {
     const int vq = quant_device_status(clear != 0);
     const int vm = moe_device_status(clear != 0);
     const int vd = dgrad_device_status(clear != 0);
-    if (vs < 0 || vq < 0 || vm < 0 || vd < 0) return W4A16_ERR_CUDA;
-    return v != 0 ? v : (vs != 0 ? vs : (vq != 0 ? vq : (vm != 0 ? vm : vd)));
+    const int vl = lora_device_status(clear != 0);
+    if (vs < 0 || vq < 0 || vm < 0 || vd < 0 || vl < 0) return W4A16_ERR_CUDA;
+    for (int x : {v, vs, vq, vm, vd})
+        if (x != 0) return x;
+    return vl;
 }
 
 extern "C" int w4a16_set_fault_injection(int64_t stall_stage, int64_t wait_limit_cycles) {

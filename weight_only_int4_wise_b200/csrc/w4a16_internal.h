@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -52,6 +53,21 @@ int moe_device_status(bool clear);
 
 // The quantiser kernel's latched device status (0 = none, -1 if it could not be read).
 int quant_device_status(bool clear);
+
+// The adapter kernel's latched device status (0 = none, -1 if it could not be read).
+int lora_device_status(bool clear);
+
+// What the shared product adds for low-rank adapters: V [M, R] fp32 (scaled
+// down-projections), LB [L, N, R], and for the tensor-core form the distinct
+// adapters of each token tile.
+struct LoraOperands {
+    const __half* LB;
+    const int32_t* ids;   // [M], negative or >= L: no adapter
+    const float* V;
+    const int32_t* list;  // [tiles][tile rows]
+    const int32_t* count; // [tiles]
+    int32_t L, R;
+};
 
 // The transposed product's latched device status (0 = none, -1 if it could not be read).
 int dgrad_device_status(bool clear);
@@ -115,5 +131,22 @@ int skinny_gated_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt
 int skinny_grouped_launch(const SkinnyPlan& plan, const void* A, const uint8_t* const* Wt, const void* const* S,
                           const int32_t* offsets, void* C, int64_t E, int64_t total_rows, int64_t N, int64_t K,
                           int64_t G, int act, cudaStream_t stream);
+
+// The product with adapters for M <= kSkinnyMaxM (plan from skinny_plan).
+int skinny_lora_launch(const SkinnyPlan& plan, const LoraOperands& lora, const void* A, const uint8_t* Wt,
+                       const void* S, void* C, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream);
+
+// How the product with adapters will launch, and the launch itself (right after
+// the kernel that makes V, on the same stream).
+struct LoraPlan {
+    bool skinny;
+    SkinnyPlan sk;
+    int tile_rows;  // token tile of the tensor-core form; 0 for the skinny form
+    int splits;
+    int grid_y, grid_z;
+};
+int lora_plan(int64_t M, int64_t N, int64_t K, int64_t G, LoraPlan* plan);
+int lora_product(const LoraPlan& plan, const LoraOperands& lora, const w4a16_half* A, const uint8_t* Wt,
+                 const w4a16_half* S, w4a16_half* C, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream);
 
 }  // namespace w4a16

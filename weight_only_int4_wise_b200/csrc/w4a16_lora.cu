@@ -1,0 +1,258 @@
+// Low-rank adapters of many requests beside one shared 4-bit projection:
+//     C[m] = fp16( A[m] W + scaling[i] * (A[m] LA[i]^T) LB[i]^T ),  i = ids[m],
+// LA [L, R, K], LB [L, N, R] fp16, one adapter index per row (negative: none).
+// (The Int4GroupwiseGemmPluginV2 page describes the shared projection only.)
+//
+// Two launches. The first, here, makes V[m, r] = scaling[i] * sum_k A[m, k]
+// LA[i, r, k] in fp32 (R values per row); the second is the shared product with
+// V LB^T added to its fp32 sums before their one rounding (w4a16_skinny.cu for
+// M <= 16, w4a16_gemm.cu above). Keeping V apart costs M * R * 4 bytes and a
+// launch, and spares every column tile of the product the R * K products of its
+// rows. The second launch starts as soon as this one's CTAs run: this kernel
+// signals its dependents only after its own wait for the previous kernel, so
+// whatever this call's caller wrote is complete by then, and the product waits
+// for this kernel only where it reads V.
+//
+// down kernel: one CTA takes 16 rows, 8 * RT ranks and one distinct adapter of
+// those rows at a time (grid y strides over them); its 16 warps split K into
+// 32-deep blocks, read both operands straight from global memory into MMA
+// fragments (16 bytes per lane: inside a block the order of k is free as long
+// as both operands use it), and add their fp32 partials in warp order through
+// shared memory. Rows of another adapter ride along and are not written. It is
+// bound by latency at decode sizes and by reading A and the adapters (L2) at
+// prompt sizes. Extra CTAs behind the row groups list the distinct adapters of
+// each token tile of the tensor-core product.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/w4a16.h"
+#include "ptx.cuh"
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+
+namespace {
+
+__device__ int g_lora_status;  // latched device-side error (0 = none)
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;
+
+struct DownParams {
+    const __half* A;
+    const __half* LA;
+    const int32_t* ids;
+    const float* scaling;  // null: 1
+    float* V;              // [M, R]
+    int32_t* list;         // [tiles][tile_rows] distinct adapters of each token tile
+    int32_t* count;        // [tiles]
+    int32_t M, K, L, R;
+    int32_t groups;        // row groups of 16; CTAs behind them make the lists
+    int32_t tile_rows;     // token tile of the product (0: no lists)
+};
+
+__device__ __forceinline__ int adapter_of(const DownParams& p, int m) {
+    if (m >= p.M) return -1;
+    const int id = p.ids[m];
+    if (id >= p.L) {
+        atomicCAS(&g_lora_status, 0, W4A16_ERR_BAD_ADAPTER);  // the row is computed without an adapter
+        return -1;
+    }
+    return id;
+}
+
+// The distinct adapters of token tile z, in the order of their first rows.
+__device__ void list_adapters(const DownParams& p, int z, int* sid, int* wcount) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int id = tid < p.tile_rows ? adapter_of(p, z * p.tile_rows + tid) : -1;
+    sid[tid] = id;
+    __syncthreads();
+    bool first = id >= 0;
+    for (int i = 0; i < tid; i += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(sid + i);
+        first = first && !((v.x == id) | (v.y == id && i + 1 < tid) | (v.z == id && i + 2 < tid) |
+                           (v.w == id && i + 3 < tid));
+    }
+    const uint32_t b = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) wcount[warp] = __popc(b);
+    __syncthreads();
+    int at = __popc(b & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) at += wcount[w];
+    if (first) p.list[static_cast<int64_t>(z) * p.tile_rows + at] = id;
+    if (tid == 0) {
+        int n = 0;
+        for (int w = 0; w < kWarps; ++w) n += wcount[w];
+        p.count[z] = n;
+    }
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p) {
+    __shared__ __align__(16) float red[kWarps * kRows * 8 * RT];
+    grid_dependency_wait();    // the operands may come from the previous kernel
+    __threadfence();
+    grid_launch_dependents();  // (only now: the product's early loads rely on that kernel being complete)
+    if (static_cast<int>(blockIdx.x) >= p.groups) {
+        if (blockIdx.y == 0 && blockIdx.z == 0)
+            list_adapters(p, blockIdx.x - p.groups, reinterpret_cast<int*>(red),
+                          reinterpret_cast<int*>(red) + kThreads);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int m0 = blockIdx.x * kRows;
+    const int r0 = blockIdx.z * 8 * RT;
+    // Distinct adapters of the group: the lowest lane of each set of equal rows.
+    const int mine = lane < kRows ? adapter_of(p, m0 + lane) : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, mine);
+    uint32_t leaders = __ballot_sync(0xffffffffu, mine >= 0 && (same & ((1u << lane) - 1u)) == 0);
+    for (int slot = 0; leaders; ++slot, leaders &= leaders - 1) {
+        if (slot % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
+        const int id = __shfl_sync(0xffffffffu, mine, __ffs(leaders) - 1);
+        float acc[RT][4];
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        const __half* a0 = p.A + static_cast<int64_t>(m0 + g) * p.K + 8 * t;
+        const __half* a1 = a0 + static_cast<int64_t>(8) * p.K;
+        const bool ok0 = m0 + g < p.M, ok1 = m0 + g + 8 < p.M;
+        const __half* lb = p.LA + (static_cast<int64_t>(id) * p.R + r0 + g) * p.K + 8 * t;
+#pragma unroll 4
+        for (int k = 32 * warp; k < p.K; k += 32 * kWarps) {
+            const bool in = k + 8 * t < p.K;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x0 = in && ok0 ? *reinterpret_cast<const uint4*>(a0 + k) : zero;
+            const uint4 x1 = in && ok1 ? *reinterpret_cast<const uint4*>(a1 + k) : zero;
+            const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y};
+            const uint32_t f1[4] = {x0.z, x1.z, x0.w, x1.w};
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const uint4 y = in && r0 + 8 * j + g < p.R
+                                    ? ld_nc_v4(lb + static_cast<int64_t>(8 * j) * p.K + k)
+                                    : zero;
+                mma_m16n8k16(acc[j], f0, y.x, y.y);
+                mma_m16n8k16(acc[j], f1, y.z, y.w);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            float* d = red + (warp * kRows + g) * 8 * RT + 8 * j + 2 * t;
+            *reinterpret_cast<float2*>(d) = make_float2(acc[j][0], acc[j][1]);
+            *reinterpret_cast<float2*>(d + 8 * 8 * RT) = make_float2(acc[j][2], acc[j][3]);
+        }
+        __syncthreads();
+        const float s = p.scaling ? p.scaling[id] : 1.f;
+        for (int o = threadIdx.x; o < kRows * 8 * RT; o += kThreads) {
+            const int m = m0 + o / (8 * RT), r = r0 + o % (8 * RT);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += red[w * kRows * 8 * RT + o];  // warp order
+            if (m < p.M && r < p.R && p.ids[m] == id) p.V[static_cast<int64_t>(m) * p.R + r] = s * sum;
+        }
+        __syncthreads();
+    }
+}
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
+
+template <int RT>
+int launch_down(const DownParams& p, dim3 grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_down_kernel<RT>, p) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
+}
+
+int lora_down(DownParams& p, int tiles, cudaStream_t stream) {
+    p.groups = (p.M + kRows - 1) / kRows;
+    // Ranks per CTA: few row groups spread the ranks over CTAs (8 each); many
+    // keep 16 or 32 together, so that A is read once per 16 or 32 ranks.
+    const int rt = p.groups <= 8 ? 1 : (p.R <= 16 ? 2 : 4);
+    const int chunks = (p.R + 8 * rt - 1) / (8 * rt);
+    // Adapters of a group side by side while the grid is below two CTAs per SM.
+    const int sms = sm_count() > 0 ? sm_count() : 148;
+    const int slots = std::max(1, std::min({kRows, static_cast<int>(p.M), 2 * sms / (p.groups * chunks)}));
+    const dim3 grid(static_cast<unsigned>(p.groups + tiles), static_cast<unsigned>(slots),
+                    static_cast<unsigned>(chunks));
+    switch (rt) {
+        case 1: return launch_down<1>(p, grid, stream);
+        case 2: return launch_down<2>(p, grid, stream);
+        default: return launch_down<4>(p, grid, stream);
+    }
+}
+
+}  // namespace
+
+int lora_device_status(bool clear) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_lora_status, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && v != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_lora_status, &zero, sizeof(int)) != cudaSuccess) return -1;
+    }
+    return v;
+}
+
+}  // namespace w4a16
+
+using namespace w4a16;
+
+extern "C" int64_t w4a16_lora_workspace_size(int64_t M, int64_t R) {
+    if (M < 0 || M >= (int64_t(1) << 31) || R < 8 || R > W4A16_MAX_RANK || R % 8) return -1;
+    // V, the tiles' lists (at most 255 rows of padding), their lengths (tiles of at least 16 rows)
+    return round256(M * R * 4) + round256((M + 256) * 4) + round256((M / 16 + 1) * 4);
+}
+
+extern "C" int w4a16_lora_gemm(const w4a16_half* A_dev, const uint8_t* Wt_dev, const w4a16_half* S_dev,
+                               const w4a16_half* LA_dev, const w4a16_half* LB_dev, const int32_t* ids_dev,
+                               const float* scaling_dev, w4a16_half* C_dev, int64_t M, int64_t N, int64_t K, int64_t G,
+                               int64_t L, int64_t R, void* workspace_dev, int64_t workspace_bytes, void* stream) {
+    if (!A_dev || !Wt_dev || !S_dev || !LA_dev || !LB_dev || !ids_dev || !C_dev || !workspace_dev || M < 0 || L < 1 ||
+        R < 1)
+        return W4A16_ERR_INVALID_ARG;
+    int rc = check_shape(N, K, G);
+    if (rc) return rc;
+    if (M >= (int64_t(1) << 31) || L >= (int64_t(1) << 31) || R % 8 || R > W4A16_MAX_RANK)
+        return W4A16_ERR_UNSUPPORTED;
+    if (workspace_bytes < w4a16_lora_workspace_size(M, R)) return W4A16_ERR_INVALID_ARG;
+    for (const void* q : {static_cast<const void*>(A_dev), static_cast<const void*>(Wt_dev),
+                          static_cast<const void*>(S_dev), static_cast<const void*>(LA_dev),
+                          static_cast<const void*>(LB_dev), static_cast<const void*>(workspace_dev)})
+        if (!aligned(q, 16)) return W4A16_ERR_MISALIGNED;
+    if (!aligned(C_dev, 2) || !aligned(ids_dev, 4) || !aligned(scaling_dev, 4)) return W4A16_ERR_MISALIGNED;
+    if (M == 0) return W4A16_OK;
+    rc = check_device();
+    if (rc) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
+    DownParams d{};
+    d.A = reinterpret_cast<const __half*>(A_dev);
+    d.LA = reinterpret_cast<const __half*>(LA_dev);
+    d.ids = ids_dev;
+    d.scaling = scaling_dev;
+    d.V = reinterpret_cast<float*>(ws);
+    d.list = reinterpret_cast<int32_t*>(ws + round256(M * R * 4));
+    d.count = reinterpret_cast<int32_t*>(ws + round256(M * R * 4) + round256((M + 256) * 4));
+    d.M = static_cast<int32_t>(M);
+    d.K = static_cast<int32_t>(K);
+    d.L = static_cast<int32_t>(L);
+    d.R = static_cast<int32_t>(R);
+    LoraOperands lora{reinterpret_cast<const __half*>(LB_dev), ids_dev, d.V, d.list, d.count, d.L, d.R};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LoraPlan plan;
+    rc = lora_plan(M, N, K, G, &plan);
+    if (rc) return rc;
+    d.tile_rows = plan.tile_rows;
+    rc = lora_down(d, plan.tile_rows ? static_cast<int>((M + plan.tile_rows - 1) / plan.tile_rows) : 0, s);
+    if (rc) return rc;
+    return lora_product(plan, lora, A_dev, Wt_dev, S_dev, C_dev, M, N, K, G, s);
+}

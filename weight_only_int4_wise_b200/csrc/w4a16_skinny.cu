@@ -75,12 +75,35 @@ struct SkinnyParams {
     const __half* sc2;
     __half* Pg;
     __half* Pu;
+    LoraOperands lora;  // adapter mode
 };
 
-// What a launch computes: the dense product, the grouped-expert product, or the
-// gated projections (separate instantiations, so that each form keeps its own
+// What a launch computes: the dense product, the grouped-expert product, the
+// gated projections, or the dense product with a low-rank adapter per row
+// (separate instantiations, so that each form keeps its own
 // register budget).
-enum SkinnyForm { kDense = 0, kGrouped = 1, kGated = 2 };
+enum SkinnyForm { kDense = 0, kGrouped = 1, kGated = 2, kLora = 3 };
+
+
+// The adapter's part of one output: sum_r V[m, r] LB[id, n, r] in fp32, 0 without an adapter.
+__device__ __forceinline__ float lora_term(const LoraOperands& l, int N, int m, int n) {
+    const int id = l.ids[m];
+    if (id < 0 || id >= l.L) return 0.f;
+    const uint4* b = reinterpret_cast<const uint4*>(l.LB + (static_cast<int64_t>(id) * N + n) * l.R);
+    const float4* v = reinterpret_cast<const float4*>(l.V + static_cast<int64_t>(m) * l.R);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < l.R / 8; ++c) {
+        const uint4 w = __ldcg(b + c);
+        const float4 x = __ldcg(v + 2 * c), y = __ldcg(v + 2 * c + 1);
+        const __half2* h = reinterpret_cast<const __half2*>(&w);
+        const float2 w0 = __half22float2(h[0]), w1 = __half22float2(h[1]);
+        const float2 w2 = __half22float2(h[2]), w3 = __half22float2(h[3]);
+        sum = fmaf(x.x, w0.x, fmaf(x.y, w0.y, fmaf(x.z, w1.x, fmaf(x.w, w1.y, sum))));
+        sum = fmaf(y.x, w2.x, fmaf(y.y, w2.y, fmaf(y.z, w3.x, fmaf(y.w, w3.y, sum))));
+    }
+    return sum;
+}
 
 // KH = 2 runs two sets of 8 warps over the same 128 columns, the first taking
 // the even 128-deep blocks of the CTA's K range and the second the odd ones, and
@@ -100,7 +123,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
     w4a16_skinny_kernel(const __grid_constant__ SkinnyParams p) {
     extern __shared__ __align__(1024) uint8_t sm[];
     constexpr int kThreads = KH * kSkThreads;
-    constexpr bool GROUPED = FORM == kGrouped, GATED = FORM == kGated;
+    constexpr bool GROUPED = FORM == kGrouped, GATED = FORM == kGated, LORA = FORM == kLora;
     constexpr int kCols = GATED ? 64 : 128;  // output columns of a CTA
     // This CTA's operands: the whole product, or in grouped mode its expert's
     // row segment (every CTA of a cluster has the same expert, so a cluster
@@ -191,7 +214,11 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
 
     // ---- with static weights (declared by the caller) the scale and weight
     // copies start before the previous kernel in the stream has finished
-    if (p.prefetch) {
+    // (Adapter form: the launch follows the kernel that makes V, which lets it start
+    // only once everything before it is complete. Its weights, scales and
+    // activations are read at once, past L1, and it waits for that kernel just
+    // before it reads V.)
+    if (LORA || p.prefetch) {
         issue_scales();
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) issue_block(i);
@@ -200,8 +227,8 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
     // ---- everything else may come from the previous kernel: wait for it, then
     // stage the activations with plain loads (zero past M and K)
     grid_launch_dependents();
-    grid_dependency_wait();
-    if (!p.prefetch) {
+    if (!LORA) grid_dependency_wait();
+    if (!LORA && !p.prefetch) {
         issue_scales();
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) issue_block(i);
@@ -226,7 +253,8 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
                 const int k = kr0 + c * 8;
                 v[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (idx0 + u * kThreads < total && r < Mrows && k < p.K)
-                    v[u] = *reinterpret_cast<const uint4*>(Ap + static_cast<int64_t>(r) * p.K + k);
+                    v[u] = LORA ? __ldcg(reinterpret_cast<const uint4*>(Ap + static_cast<int64_t>(r) * p.K + k))
+                                : *reinterpret_cast<const uint4*>(Ap + static_cast<int64_t>(r) * p.K + k);
                 c += cstep;
                 r += rstep;
                 if (c >= cpr) {
@@ -375,6 +403,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
         }
     }
 
+    if (LORA) grid_dependency_wait();  // V is complete (and the output may be written)
     const int na = nt * kCols + ja;
     // One gated output: H, and the projections if they are kept.
     auto store_gated = [&](int m, int n, float gv, float uv) {
@@ -405,6 +434,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
             for (int e = 0; e < 4; ++e) {
                 const int m = m0 + (e & 1);
                 const int n = na + ((e >> 1) << 3);
+                if (LORA && m < Mrows && n < p.N) acc[j][e] += lora_term(p.lora, p.N, m, n);
                 if (m < Mrows && n < p.N)
                     Cp[static_cast<int64_t>(m) * p.N + n] =
                         GROUPED ? epilogue_value(acc[j][e], p.act) : __float2half_rn(acc[j][e]);
@@ -461,6 +491,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
         if (n < p.N) {
             float sum = 0.f;
             for (int r = 0; r < S; ++r) sum += red[(r * MP + m) * cwm + c];
+            if (LORA) sum += lora_term(p.lora, p.N, m, n);
             Cp[static_cast<int64_t>(m) * p.N + n] = GROUPED ? epilogue_value(sum, p.act) : __float2half_rn(sum);
         }
     }
@@ -598,7 +629,7 @@ namespace {
 // Launch with filled parameters; grid z = 1 (dense) or the number of experts.
 int skinny_launch_params(const SkinnyPlan& plan, SkinnyForm form, SkinnyParams& p, int64_t N, int64_t K, int64_t G,
                          unsigned grid_z, cudaStream_t stream) {
-    constexpr int kForms = 18;
+    constexpr int kForms = 24;
     static bool attr_done[kForms][64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
@@ -614,7 +645,10 @@ int skinny_launch_params(const SkinnyPlan& plan, SkinnyForm form, SkinnyParams& 
         w4a16_skinny_kernel<2, 4, 1, kGrouped>, w4a16_skinny_kernel<2, 8, 1, kGrouped>,
         w4a16_skinny_kernel<1, 4, 1, kGated>,   w4a16_skinny_kernel<1, 8, 1, kGated>,
         w4a16_skinny_kernel<1, 2, 2, kGated>,   w4a16_skinny_kernel<1, 4, 2, kGated>,
-        w4a16_skinny_kernel<2, 4, 1, kGated>,   w4a16_skinny_kernel<2, 8, 1, kGated>};
+        w4a16_skinny_kernel<2, 4, 1, kGated>,   w4a16_skinny_kernel<2, 8, 1, kGated>,
+        w4a16_skinny_kernel<1, 4, 1, kLora>,    w4a16_skinny_kernel<1, 8, 1, kLora>,
+        w4a16_skinny_kernel<1, 2, 2, kLora>,    w4a16_skinny_kernel<1, 4, 2, kLora>,
+        w4a16_skinny_kernel<2, 4, 1, kLora>,    w4a16_skinny_kernel<2, 8, 1, kLora>};
     if (!attr_done[vi][dev]) {
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess ||
@@ -693,6 +727,19 @@ int skinny_grouped_launch(const SkinnyPlan& plan, const void* A, const uint8_t* 
     p.offsets = offsets;
     p.prefetch = 0;  // the expert of a CTA is known only after the offsets, which follow the wait
     return skinny_launch_params(plan, kGrouped, p, N, K, G, static_cast<unsigned>(E), stream);
+}
+
+int skinny_lora_launch(const SkinnyPlan& plan, const LoraOperands& lora, const void* A, const uint8_t* Wt,
+                       const void* S, void* C, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream) {
+    SkinnyParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.wt = Wt;
+    p.sc = reinterpret_cast<const __half*>(S);
+    p.A = reinterpret_cast<const __half*>(A);
+    p.C = reinterpret_cast<__half*>(C);
+    p.M = static_cast<int32_t>(M);
+    p.lora = lora;
+    return skinny_launch_params(plan, kLora, p, N, K, G, 1, stream);
 }
 
 int skinny_gated_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt_gate, const void* S_gate,
