@@ -558,73 +558,85 @@ def gemm_w8(A, wt8, S, N: int, G: int, out=None, stream=None):
     return C
 
 
-def _operand(name: str, t, dtype, shape, like):
-    """A dense CUDA operand of a given type and shape on `like`'s device (a dense copy if it is strided)."""
-    if t.device != like.device:
-        raise ValueError(f"{name} must live on {like.device}, as the other operands do")
+# The helpers below run in front of launches of a few microseconds: the checks are plain comparisons, and messages
+# are put together only for an error.
+
+def _torch_half():
+    import torch
+    return torch.float16
+
+
+def _refuse(name, t, dtype, shape, device):
+    if t.get_device() != device:
+        raise ValueError(f"{name} must live on CUDA device {device}, as the call's rows do, not on {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _operand(name, t, dtype, shape, device):
+    """A dense operand of a given type and shape on a device (a dense copy if it is strided)."""
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape:
+        _refuse(name, t, dtype, shape, device)
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _rows_operand(name: str, t):
-    """The CUDA fp16 matrix that a call's rows come from; sets the call's device."""
-    import torch
+def _rows_operand(name, t, dtype):
+    """The CUDA matrix that a call's rows come from: (device index, rows, columns)."""
     if not t.is_cuda:
-        raise ValueError("all tensors must live on a CUDA device")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {list(t.shape)}")
-    return t
+    return t.get_device(), t.shape[0], t.shape[1]
 
 
-def _weight_operand(name: str, wt, S, K: int, N: int, G: int, like):
+def _scales(name, wt, S, K, N, G, half, device):
     """Checks tiled int4 weights [K, N] against their sizes; returns the dense scales."""
-    import torch
     if G <= 0:
         raise W4A16Error(ERR_INVALID_ARG, name)
-    if (wt.device != like.device or wt.dtype != torch.uint8 or not wt.is_contiguous()
+    if (wt.get_device() != device or wt.element_size() != 1 or not wt.is_contiguous()
             or wt.numel() != ((K + 63) // 64) * ((N + 127) // 128) * 4096):
-        raise ValueError(f"{name} must be the tiled layout of [{K}, {N}] codes (dense uint8) on {like.device}")
-    return _operand(f"the scales of {name}", S, torch.float16, ((K + G - 1) // G, N), like)
+        raise ValueError(f"{name} must be the tiled layout of [{K}, {N}] codes (dense uint8) on CUDA device {device}")
+    if S.get_device() != device or S.dtype is not half or S.shape != ((K + G - 1) // G, N):
+        _refuse(f"the scales of {name}", S, half, ((K + G - 1) // G, N), device)
+    return S if S.is_contiguous() else S.contiguous()
 
 
-def _output(name: str, out, shape, like):
-    import torch
+def _output(name, out, shape, like):
     if out is None:
-        return torch.empty(shape, dtype=torch.float16, device=like.device)
-    if out.device != like.device or out.dtype != torch.float16 or out.shape != shape or not out.is_contiguous():
-        raise ValueError(f"{name} must be a dense float16 tensor of shape {list(shape)} on {like.device}")
+        return like.new_empty(shape)
+    if (out.get_device() != like.get_device() or out.dtype is not like.dtype or out.shape != shape
+            or not out.is_contiguous()):
+        raise ValueError(f"{name} must be a dense {like.dtype} tensor of shape {list(shape)} on {like.device}")
     return out
 
 
 class _launch_on:
-    """The device of `tensor` and, if one is given, `stream` (a torch stream or a raw handle) made current for one
-    call, so that the copies and buffers that the call makes belong to the stream its kernels run on. Yields the
-    stream's raw handle."""
+    """A device and, if one is given, a stream (a torch stream or a raw handle) made current for one call, so that
+    the copies and buffers that the call makes belong to the stream its kernels run on. Yields the stream's raw
+    handle."""
 
-    __slots__ = ("index", "stream", "guards")
+    __slots__ = ("device", "stream", "guards")
 
-    def __init__(self, tensor, stream):
-        self.index, self.stream, self.guards = tensor.device.index, stream, ()
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, ()
 
     def __enter__(self):
         import torch
-        if self.stream is None and self.index == torch.cuda.current_device():
-            return _current_stream(self.index)
-        self.guards = [torch.cuda.device(self.index)]
+        if self.stream is None and self.device == torch.cuda.current_device():
+            return _current_stream(self.device)
+        self.guards = [torch.cuda.device(self.device)]
         self.guards[0].__enter__()
-        if self.stream is not None:
-            raw = _stream(self.stream)
-            st = self.stream if isinstance(self.stream, torch.cuda.Stream) else (
-                torch.cuda.ExternalStream(raw, device=self.index) if raw else torch.cuda.default_stream(self.index))
-            self.guards.append(torch.cuda.stream(st))
-            self.guards[1].__enter__()
-            return raw
-        return _current_stream(self.index)
+        if self.stream is None:
+            return _current_stream(self.device)
+        raw = _stream(self.stream)
+        st = self.stream if isinstance(self.stream, torch.cuda.Stream) else (
+            torch.cuda.ExternalStream(raw, device=self.device) if raw else torch.cuda.default_stream(self.device))
+        self.guards.append(torch.cuda.stream(st))
+        self.guards[1].__enter__()
+        return raw
 
     def __exit__(self, *exc):
         for guard in reversed(self.guards):
@@ -637,11 +649,12 @@ def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_S
     """H [M, N] fp16 = act(A x W_gate) * (A x W_up) from activations A [M, K] fp16 and two tiled weight
     matrices [K, N] with scales [ceil(K/G), N]; one rounding. With save=True returns (H, gate, up), the two
     projections in fp16 as gated_gemm_backward reads them."""
-    M, K = _rows_operand("A", A).shape
-    with _launch_on(A, stream) as st:
+    half = _torch_half()
+    device, M, K = _rows_operand("A", A, half)
+    with _launch_on(device, stream) as st:
         A = A if A.is_contiguous() else A.contiguous()
-        S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, A)
-        S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, A)
+        S_gate = _scales("wt_gate", wt_gate, S_gate, K, N, G, half, device)
+        S_up = _scales("wt_up", wt_up, S_up, K, N, G, half, device)
         H = _output("out", out, (M, N), A)
         Pg = _output("out_gate", out_gate, (M, N), A) if save else None
         Pu = _output("out_up", out_up, (M, N), A) if save else None
@@ -658,10 +671,11 @@ def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_S
 def gemm_dgrad(dC, wt, S, K: int, G: int, out=None, flags: int = 0, stream=None):
     """dA [M, K] fp16 = dC [M, N] x W^T, the gradient of gemm's input, from the forward product's tiled weights
     and scales [ceil(K/G), N]."""
-    M, N = _rows_operand("dC", dC).shape
-    with _launch_on(dC, stream) as st:
+    half = _torch_half()
+    device, M, N = _rows_operand("dC", dC, half)
+    with _launch_on(device, stream) as st:
         dC = dC if dC.is_contiguous() else dC.contiguous()
-        S = _weight_operand("wt", wt, S, K, N, G, dC)
+        S = _scales("wt", wt, S, K, N, G, half, device)
         dA = _output("out", out, (M, K), dC)
         if M:
             rc = (_lib or load()).w4a16_gemm_dgrad(dC.data_ptr(), wt.data_ptr(), S.data_ptr(), dA.data_ptr(), M, N,
@@ -675,14 +689,14 @@ def gated_gemm_backward(dH, gate, up, wt_gate, S_gate, wt_up, S_up, K: int, G: i
                         out_gate=None, out_up=None, flags: int = 0, stream=None):
     """Backward of gated_gemm with frozen weights: (dA [M, K], d_gate [M, N], d_up [M, N]) from the gradient dH
     [M, N] and the projections that gated_gemm(..., save=True) returned."""
-    import torch
-    M, N = _rows_operand("dH", dH).shape
-    with _launch_on(dH, stream) as st:
+    half = _torch_half()
+    device, M, N = _rows_operand("dH", dH, half)
+    with _launch_on(device, stream) as st:
         dH = dH if dH.is_contiguous() else dH.contiguous()
-        gate = _operand("gate", gate, torch.float16, (M, N), dH)
-        up = _operand("up", up, torch.float16, (M, N), dH)
-        S_gate = _weight_operand("wt_gate", wt_gate, S_gate, K, N, G, dH)
-        S_up = _weight_operand("wt_up", wt_up, S_up, K, N, G, dH)
+        gate = _operand("gate", gate, half, (M, N), device)
+        up = _operand("up", up, half, (M, N), device)
+        S_gate = _scales("wt_gate", wt_gate, S_gate, K, N, G, half, device)
+        S_up = _scales("wt_up", wt_up, S_up, K, N, G, half, device)
         dA = _output("out", out, (M, K), dH)
         dG, dU = _output("out_gate", out_gate, (M, N), dH), _output("out_up", out_up, (M, N), dH)
         if M:
@@ -701,25 +715,26 @@ def lora_gemm(A, wt, S, N: int, G: int, lora_A, lora_B, ids, scaling=None, works
     int32 and scaling [L] float32 (None: 1) on the device. The workspace (uint8, w4a16_lora_workspace_size(M, R)
     bytes) is allocated here when not given."""
     import torch
-    M, K = _rows_operand("A", A).shape
+    half = torch.float16
+    device, M, K = _rows_operand("A", A, half)
     if lora_A.dim() != 3:
         raise ValueError(f"lora_A must be [L, R, K], got {list(lora_A.shape)}")
     L, R = lora_A.shape[0], lora_A.shape[1]
-    with _launch_on(A, stream) as st:
+    with _launch_on(device, stream) as st:
         A = A if A.is_contiguous() else A.contiguous()
-        S = _weight_operand("wt", wt, S, K, N, G, A)
-        lora_A = _operand("lora_A", lora_A, torch.float16, (L, R, K), A)
-        lora_B = _operand("lora_B", lora_B, torch.float16, (L, N, R), A)
-        ids = _operand("ids", ids, torch.int32, (M,), A)
+        S = _scales("wt", wt, S, K, N, G, half, device)
+        lora_A = _operand("lora_A", lora_A, half, (L, R, K), device)
+        lora_B = _operand("lora_B", lora_B, half, (L, N, R), device)
+        ids = _operand("ids", ids, torch.int32, (M,), device)
         if scaling is not None:
-            scaling = _operand("scaling", scaling, torch.float32, (L,), A)
+            scaling = _operand("scaling", scaling, torch.float32, (L,), device)
         C = _output("out", out, (M, N), A)
         if M:
             lib = _lib or load()
             need = lib.w4a16_lora_workspace_size(M, R)
             if workspace is None:
-                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=A.device)
-            elif workspace.device != A.device or not workspace.is_contiguous():
+                workspace = A.new_empty(max(need, 2) // 2)  # (2-byte elements; the size is a multiple of 256)
+            elif workspace.get_device() != device or not workspace.is_contiguous():
                 raise ValueError(f"the workspace must be a dense tensor on {A.device}")
             rc = lib.w4a16_lora_gemm(A.data_ptr(), wt.data_ptr(), S.data_ptr(), lora_A.data_ptr(), lora_B.data_ptr(),
                                      ids.data_ptr(), None if scaling is None else scaling.data_ptr(), C.data_ptr(),
