@@ -351,9 +351,8 @@ int w4a16_gated_gemm_backward(const w4a16_half* dH_dev, const w4a16_half* Pg_dev
  * one adapter need not be neighbours. An index not below L latches
  * W4A16_ERR_BAD_ADAPTER and its row is computed without an adapter.
  * Sums are fp32 and C is rounded once. V = scaling * A LA^T must stay within
- * fp16's range: for M > 16 it is rounded to fp16 before its product with LB (a
- * further 2^-12 of the adapter's part, like the weights' own rounding). For M <=
- * 16 the shared part is scaled as w4a16_gemm does it. A row's values never
+ * fp16's range: it is rounded to fp16 before its product with LB (up to 2^-11
+ * of the adapter's part, as the weights' own rounding). A row's values never
  * reach another row's output, and neither does an infinity or NaN in the LB of an
  * adapter that the row does not use.
  * R a multiple of 8 up to W4A16_MAX_RANK, 1 <= L < 2^31. workspace_dev:

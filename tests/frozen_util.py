@@ -111,22 +111,18 @@ def gated_backward(dH, g, u, Wg, Wu, a):
     return (dA, dG, dU), (half_step(dA) + 1.001 * eA, eG, eU)
 
 
-def lora(A, W, LA, LB, ids, scaling, V_bits: int, exact_shared: bool):
-    """The product with one adapter per row, and the bound of its fp16 result's error. V_bits: bits of the
-    rounding of V (11: fp16 before its product, 24: kept in 32 bits). exact_shared: whether the shared weights enter
-    as fp16(q * s); otherwise they enter as q * s (scaled after the sum), which differs by half an fp16 step each."""
+def lora(A, W, LA, LB, ids, scaling):
+    """The product with one adapter per row, and the bound of its fp16 result's error: V = scaling * A LA^T is
+    rounded to fp16 before its product."""
     A64 = A.astype(np.float64)
     C, e = product(A, W)
-    if not exact_shared:
-        e = e + np.abs(A64) @ (np.abs(W) * 2.0 ** -11)
-    C, e = C.copy(), e.copy()
     for m, i in enumerate(ids):
         if not 0 <= i < LA.shape[0]:
             continue
         a, b, s = LA[i].astype(np.float64), LB[i].astype(np.float64), float(scaling[i])
         v = s * (a @ A64[m])
         ev = sum_error(A.shape[1], abs(s) * (np.abs(a) @ np.abs(A64[m]))) + np.abs(v) * 2.0 ** -24
-        ev = ev + np.maximum(np.abs(v) * 2.0 ** -V_bits, 2.0 ** -25)
+        ev = ev + half_step(np.abs(v) + ev)
         C[m] += b @ v
         e[m] += np.abs(b) @ ev + sum_error(LA.shape[1], np.abs(b) @ np.abs(v))
     return C, half_step(C) + 1.001 * e

@@ -83,7 +83,7 @@ def test_lora_rejects_bad_arguments_on_host():
 def test_lora_workspace_size():
     r = lambda b: (b + 255) // 256 * 256
     for M, R in [(0, 8), (1, 16), (16, 64), (2048, 128)]:
-        assert w.w4a16_lora_workspace_size(M, R) == r(M * R * 4) + r((M + 256) * 4) + r((M // 16 + 1) * 4)
+        assert w.w4a16_lora_workspace_size(M, R) == r(M * R * 2) + r((M + 256) * 4) + r((M // 16 + 1) * 4)
     assert w.w4a16_lora_workspace_size(4, 12) == -1 and w.w4a16_lora_workspace_size(4, w.MAX_RANK + 8) == -1
     assert w.w4a16_lora_workspace_size(-1, 16) == -1
     assert w.status_string(w.ERR_BAD_ADAPTER) != "unknown status"

@@ -42,8 +42,7 @@ class Case:
         return out
 
     def reference(self):
-        small = self.M <= 16
-        return f.lora(self.A, self.W, self.LA, self.LB, self.ids, self.scaling, 24 if small else 11, not small)
+        return f.lora(self.A, self.W, self.LA, self.LB, self.ids, self.scaling)
 
     def check(self):
         flat, out, pad = guarded_output(self.M, self.N)
@@ -92,12 +91,10 @@ def test_no_scaling_means_one():
 
 
 def test_rows_without_adapter_equal_the_plain_product():
-    for M in (1, 16, 300):  # (launch forms that split K alike: the sums have one order)
-        c = Case(M, 512, 264, 128, 3, 16, seed=M)
-        plain = w.gemm(dev(c.A), c.wt, dev(c.S), c.N, c.G)
-        got = c.run()
-        none = c.ids < 0
-        assert torch.equal(got[none], plain[none])
+    c = Case(300, 512, 264, 128, 3, 16, seed=300)  # (the same kernel without a K split: one order of the sums)
+    plain = w.gemm(dev(c.A), c.wt, dev(c.S), c.N, c.G)
+    none = c.ids < 0
+    assert torch.equal(c.run()[none], plain[none])
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])

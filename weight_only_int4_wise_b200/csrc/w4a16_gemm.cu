@@ -538,13 +538,8 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
                         const int d = (q0 + q) / per, rr = (q0 + q) - d * per;
                         uint4 x = make_uint4(0u, 0u, 0u, 0u);
                         if (d < used && id >= 0 && __ldcg(list + d) == id) {
-                            const float4* src =
-                                reinterpret_cast<const float4*>(p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R + 8 * rr);
-                            const float4 a = __ldcg(src), b = __ldcg(src + 1);
-                            x.x = h2_bits(__floats2half2_rn(a.x, a.y));
-                            x.y = h2_bits(__floats2half2_rn(a.z, a.w));
-                            x.z = h2_bits(__floats2half2_rn(b.x, b.y));
-                            x.w = h2_bits(__floats2half2_rn(b.z, b.w));
+                            x = __ldcg(reinterpret_cast<const uint4*>(
+                                p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R + 8 * rr));
                         }
                         sts128(dst + ((q ^ (row & 7)) << 4), x);
                     }
@@ -578,7 +573,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
                 for (int rr = 0; rr < p.lora.R; ++rr) {
                     const float x = __half2float(__ldcg(b + rr));
                     if (!isfinite(x))
-                        acc += __half2float(__float2half_rn(__ldcg(p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R + rr))) * x;
+                        acc += __half2float(__ldcg(p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R + rr)) * x;
                 }
                 v[t] = __float_as_uint(__uint_as_float(v[t]) + acc);
             }
@@ -1479,8 +1474,7 @@ namespace w4a16 {
 
 int lora_plan(int64_t M, int64_t N, int64_t K, int64_t G, LoraPlan* plan) {
     plan->tile_rows = 0;
-    plan->skinny = skinny_plan(M, N, K, G, &plan->sk) == W4A16_OK;
-    if (plan->skinny) return W4A16_OK;
+    if (M <= kSkinnyMaxM) return W4A16_OK;
     Plan tc;
     const int rc = plan_dense(M, N, K, &tc, true, 0, 0, kLoraInt4);
     if (rc) return rc;
@@ -1494,7 +1488,7 @@ int lora_plan(int64_t M, int64_t N, int64_t K, int64_t G, LoraPlan* plan) {
 int lora_product(const LoraPlan& plan, const LoraOperands& lora, const w4a16_half* A, const uint8_t* Wt,
                  const w4a16_half* S, w4a16_half* C, int64_t M, int64_t N, int64_t K, int64_t G,
                  cudaStream_t stream) {
-    if (plan.skinny) return skinny_lora_launch(plan.sk, lora, A, Wt, S, C, M, N, K, G, stream);
+    if (plan.tile_rows == 0) return decode_lora_launch(lora, A, Wt, S, C, M, N, K, G, stream);
     Params p;
     std::memset(&p, 0, sizeof(p));
     p.wt[0] = Wt;
@@ -1526,10 +1520,8 @@ namespace {
 int gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate, const w4a16_half* S_gate, const uint8_t* Wt_up,
                const w4a16_half* S_up, w4a16_half* H_dev, w4a16_half* Pg_dev, w4a16_half* Pu_dev, int64_t M, int64_t N,
                int64_t K, int64_t G, int act, cudaStream_t stream) {
-    SkinnyPlan sk;
-    if (skinny_plan_gated(M, N, K, G, &sk) == W4A16_OK)
-        return skinny_gated_launch(sk, A_dev, Wt_gate, S_gate, Wt_up, S_up, H_dev, Pg_dev, Pu_dev, M, N, K, G, act,
-                                   stream);
+    if (M <= kSkinnyMaxM)
+        return decode_gated_launch(A_dev, Wt_gate, S_gate, Wt_up, S_up, H_dev, Pg_dev, Pu_dev, M, N, K, G, act, stream);
     Plan plan;
     int rc = plan_dense(M, N, K, &plan, true, 0, 0, kGatedInt4);
     if (rc) return rc;

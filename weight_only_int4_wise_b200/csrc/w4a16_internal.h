@@ -57,13 +57,13 @@ int quant_device_status(bool clear);
 // The adapter kernel's latched device status (0 = none, -1 if it could not be read).
 int lora_device_status(bool clear);
 
-// What the shared product adds for low-rank adapters: V [M, R] fp32 (scaled
+// What the shared product adds for low-rank adapters: V [M, R] fp16 (scaled
 // down-projections), LB [L, N, R], and for the tensor-core form the distinct
 // adapters of each token tile.
 struct LoraOperands {
     const __half* LB;
     const int32_t* ids;   // [M], negative or >= L: no adapter
-    const float* V;
+    const __half* V;
     const int32_t* list;  // [tiles][tile rows]
     const int32_t* count; // [tiles]
     int32_t L, R;
@@ -115,12 +115,18 @@ int skinny_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt, cons
 // activations fit (the experts' column tiles already fill the grid).
 int skinny_plan_grouped(int64_t total_rows, int64_t N, int64_t K, int64_t G, SkinnyPlan* plan);
 
-// The skinny plan and launch of the gated projections (M <= kSkinnyMaxM): H
-// [M, N], and the projections Pg and Pu if not null.
-int skinny_plan_gated(int64_t M, int64_t N, int64_t K, int64_t G, SkinnyPlan* plan);
-int skinny_gated_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt_gate, const void* S_gate,
-                        const uint8_t* Wt_up, const void* S_up, void* H, void* Pg, void* Pu, int64_t M, int64_t N,
-                        int64_t K, int64_t G, int act, cudaStream_t stream);
+// The decode-sized forms (M <= kSkinnyMaxM) of the gated projections (H [M, N],
+// and the projections Pg and Pu if not null) and of the product with adapters
+// (right after the kernel that makes V, on the same stream).
+int decode_gated_launch(const void* A, const uint8_t* Wt_gate, const void* S_gate, const uint8_t* Wt_up,
+                        const void* S_up, void* H, void* Pg, void* Pu, int64_t M, int64_t N, int64_t K, int64_t G,
+                        int act, cudaStream_t stream);
+int decode_lora_launch(const LoraOperands& lora, const void* A, const uint8_t* Wt, const void* S, void* C, int64_t M,
+                       int64_t N, int64_t K, int64_t G, cudaStream_t stream);
+
+// The multiplier of floor(k / G) = (k * magic) >> 32 for every k < kend that is a
+// multiple of 8, or 0 if there is none.
+uint32_t group_magic(int64_t G, int64_t kend);
 
 // Grouped-expert form of the skinny kernel (grid z = expert) for at most 16
 // gathered rows in total (plan from skinny_plan_grouped): rows
@@ -132,16 +138,10 @@ int skinny_grouped_launch(const SkinnyPlan& plan, const void* A, const uint8_t* 
                           const int32_t* offsets, void* C, int64_t E, int64_t total_rows, int64_t N, int64_t K,
                           int64_t G, int act, cudaStream_t stream);
 
-// The product with adapters for M <= kSkinnyMaxM (plan from skinny_plan).
-int skinny_lora_launch(const SkinnyPlan& plan, const LoraOperands& lora, const void* A, const uint8_t* Wt,
-                       const void* S, void* C, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream);
-
 // How the product with adapters will launch, and the launch itself (right after
 // the kernel that makes V, on the same stream).
 struct LoraPlan {
-    bool skinny;
-    SkinnyPlan sk;
-    int tile_rows;  // token tile of the tensor-core form; 0 for the skinny form
+    int tile_rows;  // token tile of the tensor-core form; 0 for the decode-sized form
     int splits;
     int grid_y, grid_z;
 };

@@ -4,9 +4,11 @@
 // (The Int4GroupwiseGemmPluginV2 page describes the shared projection only.)
 //
 // Two launches. The first, here, makes V[m, r] = scaling[i] * sum_k A[m, k]
-// LA[i, r, k] in fp32 (R values per row); the second is the shared product with
-// V LB^T added to its fp32 sums before their one rounding (w4a16_skinny.cu for
-// M <= 16, w4a16_gemm.cu above). Keeping V apart costs M * R * 4 bytes and a
+// LA[i, r, k], summed in fp32 and rounded to fp16, the MMA's operand type (2^-12
+// of the adapter's part, as every weight of it already carries); the second is the
+// shared product with V LB^T added to its fp32 sums before their one rounding
+// (w4a16_decode.cu for M <= 16, w4a16_gemm.cu above). Keeping V apart costs M * R *
+// 2 bytes and a
 // launch, and spares every column tile of the product the R * K products of its
 // rows. The second launch starts as soon as this one's CTAs run: this kernel
 // signals its dependents only after its own wait for the previous kernel, so
@@ -47,7 +49,7 @@ struct DownParams {
     const __half* LA;
     const int32_t* ids;
     const float* scaling;  // null: 1
-    float* V;              // [M, R]
+    __half* V;             // [M, R]
     int32_t* list;         // [tiles][tile_rows] distinct adapters of each token tile
     int32_t* count;        // [tiles]
     int32_t M, K, L, R;
@@ -149,7 +151,8 @@ __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p)
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) sum += red[w * kRows * 8 * RT + o];  // warp order
-            if (m < p.M && r < p.R && p.ids[m] == id) p.V[static_cast<int64_t>(m) * p.R + r] = s * sum;
+            if (m < p.M && r < p.R && p.ids[m] == id) 
+                p.V[static_cast<int64_t>(m) * p.R + r] = __float2half_rn(s * sum);
         }
         __syncthreads();
     }
@@ -210,7 +213,7 @@ using namespace w4a16;
 extern "C" int64_t w4a16_lora_workspace_size(int64_t M, int64_t R) {
     if (M < 0 || M >= (int64_t(1) << 31) || R < 8 || R > W4A16_MAX_RANK || R % 8) return -1;
     // V, the tiles' lists (at most 255 rows of padding), their lengths (tiles of at least 16 rows)
-    return round256(M * R * 4) + round256((M + 256) * 4) + round256((M / 16 + 1) * 4);
+    return round256(M * R * 2) + round256((M + 256) * 4) + round256((M / 16 + 1) * 4);
 }
 
 extern "C" int w4a16_lora_gemm(const w4a16_half* A_dev, const uint8_t* Wt_dev, const w4a16_half* S_dev,
@@ -239,9 +242,9 @@ extern "C" int w4a16_lora_gemm(const w4a16_half* A_dev, const uint8_t* Wt_dev, c
     d.LA = reinterpret_cast<const __half*>(LA_dev);
     d.ids = ids_dev;
     d.scaling = scaling_dev;
-    d.V = reinterpret_cast<float*>(ws);
-    d.list = reinterpret_cast<int32_t*>(ws + round256(M * R * 4));
-    d.count = reinterpret_cast<int32_t*>(ws + round256(M * R * 4) + round256((M + 256) * 4));
+    d.V = reinterpret_cast<__half*>(ws);
+    d.list = reinterpret_cast<int32_t*>(ws + round256(M * R * 2));
+    d.count = reinterpret_cast<int32_t*>(ws + round256(M * R * 2) + round256((M + 256) * 4));
     d.M = static_cast<int32_t>(M);
     d.K = static_cast<int32_t>(K);
     d.L = static_cast<int32_t>(L);

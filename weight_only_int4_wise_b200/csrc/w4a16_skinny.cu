@@ -43,7 +43,6 @@ namespace {
 constexpr int kSkWarps = 8;                       // 8 warps x 16 columns = one 128-column weight tile
 constexpr int kSkThreads = kSkWarps * 32;         // threads of one K half
 constexpr int kBlockK = 128;
-constexpr int kMaxSmem = 200 * 1024;              // dynamic shared memory a launch may ask for
 constexpr int kSlotBytes = 32;                    // per thread and block: two 16-byte chunks
 
 // No wait in this kernel can fail to end (cp.async groups and cluster barriers
@@ -65,66 +64,22 @@ struct SkinnyParams {
     int32_t prefetch;         // weights/scales may be read before the previous kernel finishes
     // Grouped-expert mode (grid z = expert): rows [off[e], off[e+1]) of A and C
     // use expert e's weights and scales; M is then the total row count.
-    int32_t E, act;         // act: W4A16_ACT_* applied to the fp16 result (gated: to the gate)
+    int32_t grouped, E, act;  // act: W4A16_ACT_* applied to the fp16 result
     const int32_t* offsets;
     const uint8_t* wte[W4A16_MAX_EXPERTS];
     const __half* sce[W4A16_MAX_EXPERTS];
-    // Gated mode: wt / sc are the gate's, wt2 / sc2 the up projection's; C is H,
-    // and Pg / Pu (both or neither) take the projections themselves.
-    const uint8_t* wt2;
-    const __half* sc2;
-    __half* Pg;
-    __half* Pu;
-    LoraOperands lora;  // adapter mode
 };
-
-// What a launch computes: the dense product, the grouped-expert product, the
-// gated projections, or the dense product with a low-rank adapter per row
-// (separate instantiations, so that each form keeps its own
-// register budget).
-enum SkinnyForm { kDense = 0, kGrouped = 1, kGated = 2, kLora = 3 };
-
-
-// The adapter's part of one output: sum_r V[m, r] LB[id, n, r] in fp32, 0 without an adapter.
-__device__ __forceinline__ float lora_term(const LoraOperands& l, int N, int m, int n) {
-    const int id = l.ids[m];
-    if (id < 0 || id >= l.L) return 0.f;
-    const uint4* b = reinterpret_cast<const uint4*>(l.LB + (static_cast<int64_t>(id) * N + n) * l.R);
-    const float4* v = reinterpret_cast<const float4*>(l.V + static_cast<int64_t>(m) * l.R);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < l.R / 8; ++c) {
-        const uint4 w = __ldcg(b + c);
-        const float4 x = __ldcg(v + 2 * c), y = __ldcg(v + 2 * c + 1);
-        const __half2* h = reinterpret_cast<const __half2*>(&w);
-        const float2 w0 = __half22float2(h[0]), w1 = __half22float2(h[1]);
-        const float2 w2 = __half22float2(h[2]), w3 = __half22float2(h[3]);
-        sum = fmaf(x.x, w0.x, fmaf(x.y, w0.y, fmaf(x.z, w1.x, fmaf(x.w, w1.y, sum))));
-        sum = fmaf(y.x, w2.x, fmaf(y.y, w2.y, fmaf(y.z, w3.x, fmaf(y.w, w3.y, sum))));
-    }
-    return sum;
-}
 
 // KH = 2 runs two sets of 8 warps over the same 128 columns, the first taking
 // the even 128-deep blocks of the CTA's K range and the second the odd ones, and
 // adds the two partial tiles in shared memory (first + second) after the loop.
-//
-// FORM kGated: the CTA owns 64 output columns, and the 16 rows of a warp's MMA
-// operand are 8 gate columns (rows 0..7) and the same 8 up columns (rows 8..15).
-// One thread then holds both projections of an output (accumulators 0, 1 and 2,
-// 3), so the activation and the product need no exchange, and the weight stream,
-// staging and reduction are those of a dense product twice as wide. Each weight
-// is q*s rounded to fp16 before the MMA (the dense form scales fp32 block
-// partials instead): the product of two projections would show the difference
-// of the two roundings, 1.6 times the output's own rounding in the 2-norm
-// against 1.0.
-template <int MT, int kDepth, int KH, int FORM>
+// GROUPED: the grouped-expert form (a separate instantiation, so that the
+// dense kernels keep their register budget).
+template <int MT, int kDepth, int KH, bool GROUPED>
 __global__ void __launch_bounds__(KH * kSkThreads, 2)
     w4a16_skinny_kernel(const __grid_constant__ SkinnyParams p) {
     extern __shared__ __align__(1024) uint8_t sm[];
     constexpr int kThreads = KH * kSkThreads;
-    constexpr bool GROUPED = FORM == kGrouped, GATED = FORM == kGated, LORA = FORM == kLora;
-    constexpr int kCols = GATED ? 64 : 128;  // output columns of a CTA
     // This CTA's operands: the whole product, or in grouped mode its expert's
     // row segment (every CTA of a cluster has the same expert, so a cluster
     // leaves together).
@@ -162,8 +117,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
     const int krange = nb * kBlockK;
     constexpr int MP = 8 * MT;                      // token rows, padded to the MMA's 8-column tiles
     const int S = p.splits;
-    // widest slice of one cluster rank, in MMA rows (gated: whole gate-up pairs)
-    const int cwm = GATED ? 2 * ((64 + S - 1) / S) : (128 + S - 1) / S;
+    const int cwm = (128 + S - 1) / S;              // widest output-column slice of one cluster rank
 
     __half* act = reinterpret_cast<__half*>(sm);                          // [MP][act_stride]
     __half* scl = act + MP * p.act_stride;                                // [scale_rows][128]
@@ -173,17 +127,11 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
     const int g_lo = kr0 / p.G;
     const int g_hi = min(p.ngroups - 1, (kr0 + krange - 1) / p.G);
     const int nrows = g_hi - g_lo + 1;
-    // This thread's two MMA rows read scale columns ja and jb of the staged window:
-    // weight columns ja and ja + 8, or gate and up of column warp * 8 + g.
-    const int ja = GATED ? warp * 8 + g : warp * 16 + g;
-    const int jb = GATED ? 64 + ja : ja + 8;
+    const int ja = warp * 16 + g;  // this thread's columns: ja and ja + 8
 
     // This thread's chunk t of columns ja and ja + 8 in block i: tile 2(b0+i) + t/2,
     // half t%2. A missing second tile at an odd end of K reads as zeros.
-    const int64_t wtile = static_cast<int64_t>(GATED ? nt >> 1 : nt) * p.KT + 2 * b0 + (t >> 1);
-    const int64_t woff = wtile * 4096 + (t & 1) * 2048 + (GATED ? (nt & 1) * 64 + ja : ja) * 16;
-    const uint8_t* wsrc = Wt + woff;
-    const uint8_t* wsrc2 = GATED ? p.wt2 + woff : wsrc + 128;
+    const uint8_t* wsrc = Wt + (static_cast<int64_t>(nt) * p.KT + 2 * b0 + (t >> 1)) * 4096 + (t & 1) * 2048 + ja * 16;
     const int kt_last_ok = p.KT - 1 - (t >> 1);
     uint8_t* myslot = ring + threadIdx.x * 16;  // chunk of column ja; column ja + 8's is kThreads * 16 further
     // Local block li of this half is block i = li * KH + kh, in slot li % kDepth.
@@ -194,31 +142,24 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
             const uint8_t* src = wsrc + static_cast<int64_t>(i) * 8192;
             uint8_t* dst = myslot + (li % kDepth) * kThreads * kSlotBytes;
             cp_async16(dst, ok ? src : Wt, ok ? 16u : 0u);
-            cp_async16(dst + kThreads * 16, ok ? (GATED ? wsrc2 + static_cast<int64_t>(i) * 8192 : src + 128) : Wt,
-                       ok ? 16u : 0u);
+            cp_async16(dst + kThreads * 16, ok ? src + 128 : Wt, ok ? 16u : 0u);
         }
         cp_async_commit();  // one group per block, empty past the end, so the counts stay uniform
     };
     auto issue_scales = [&]() {
-        const int ncols = min(kCols, p.N - nt * kCols);
+        const int ncols = min(128, p.N - nt * 128);
         for (int idx = threadIdx.x; idx < nrows * 16; idx += kThreads) {
             const int r = idx >> 4, c = idx & 15;
-            const int cc = GATED ? c & 7 : c;  // gated: 8 chunks of the gate's scales, then 8 of the up projection's
-            const __half* src = GATED && c >= 8 ? p.sc2 : Sc;
-            const bool ok = cc * 8 < ncols;
+            const bool ok = c * 8 < ncols;
             cp_async16(scl + r * 128 + c * 8,
-                       ok ? src + static_cast<int64_t>(g_lo + r) * p.N + nt * kCols + cc * 8 : Sc, ok ? 16u : 0u);
+                       ok ? Sc + static_cast<int64_t>(g_lo + r) * p.N + nt * 128 + c * 8 : Sc, ok ? 16u : 0u);
         }
         cp_async_commit();  // the oldest group: complete by the time block 0 is
     };
 
     // ---- with static weights (declared by the caller) the scale and weight
     // copies start before the previous kernel in the stream has finished
-    // (Adapter form: the launch follows the kernel that makes V, which lets it start
-    // only once everything before it is complete. Its weights, scales and
-    // activations are read at once, past L1, and it waits for that kernel just
-    // before it reads V.)
-    if (LORA || p.prefetch) {
+    if (p.prefetch) {
         issue_scales();
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) issue_block(i);
@@ -227,8 +168,8 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
     // ---- everything else may come from the previous kernel: wait for it, then
     // stage the activations with plain loads (zero past M and K)
     grid_launch_dependents();
-    if (!LORA) grid_dependency_wait();
-    if (!LORA && !p.prefetch) {
+    grid_dependency_wait();
+    if (!p.prefetch) {
         issue_scales();
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) issue_block(i);
@@ -253,8 +194,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
                 const int k = kr0 + c * 8;
                 v[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (idx0 + u * kThreads < total && r < Mrows && k < p.K)
-                    v[u] = LORA ? __ldcg(reinterpret_cast<const uint4*>(Ap + static_cast<int64_t>(r) * p.K + k))
-                                : *reinterpret_cast<const uint4*>(Ap + static_cast<int64_t>(r) * p.K + k);
+                    v[u] = *reinterpret_cast<const uint4*>(Ap + static_cast<int64_t>(r) * p.K + k);
                 c += cstep;
                 r += rstep;
                 if (c >= cpr) {
@@ -304,7 +244,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
         const uint32_t kb2 = static_cast<uint32_t>(i * kBlockK * 2);  // block offset in the staged range, bytes
         const uint32_t wa_w[4] = {wa.x, wa.y, wa.z, wa.w};
         const uint32_t wb_w[4] = {wb.x, wb.y, wb.z, wb.w};
-        if (!GATED && p.post_scale) {
+        if (p.post_scale) {
             // One group covers the whole block: MMA chains over the exact codes,
             // started from zero accumulators, then one scaled add per element.
             // Two chains (even and odd 16-deep steps) halve the dependent MMA
@@ -331,7 +271,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
             const int gr =
                 static_cast<int>((static_cast<uint64_t>(kr0 + i * kBlockK) * p.g_magic) >> 32) - g_lo;  // floor(k / G)
             const float sa = __half2float(scl[gr * 128 + ja]);
-            const float sb = __half2float(scl[gr * 128 + jb]);
+            const float sb = __half2float(scl[gr * 128 + ja + 8]);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 acc[j][0] = fmaf(part[0][j][0] + part[1][j][0], sa, acc[j][0]);
@@ -340,27 +280,14 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
                 acc[j][3] = fmaf(part[0][j][3] + part[1][j][3], sb, acc[j][3]);
             }
         } else {
-            // Groups finer than the block, and every gated form: scale each decoded
-            // word (rounded to fp16); the scales are read once per block if one
-            // group covers it.
-            __half2 s2a, s2b;
-            if (GATED && p.post_scale) {
-                const int gr =
-                    static_cast<int>((static_cast<uint64_t>(kr0 + i * kBlockK) * p.g_magic) >> 32) - g_lo;
-                s2a = __half2half2(scl[gr * 128 + ja]);
-                s2b = __half2half2(scl[gr * 128 + jb]);
-            }
+            // Groups finer than the block: scale each decoded word (rounded to fp16).
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                if (!GATED || !p.post_scale) {
-                    const uint32_t kk = static_cast<uint32_t>(kr0 + i * kBlockK + 32 * t + 8 * w);
-                    const int gr =
-                        min(static_cast<int>((static_cast<uint64_t>(kk) * p.g_magic) >> 32), p.ngroups - 1) - g_lo;
-                    s2a = __half2half2(scl[gr * 128 + ja]);
-                    s2b = __half2half2(scl[gr * 128 + jb]);
-                }
-                const uint4 qa = dequant_word(wa_w[w], s2a);
-                const uint4 qb = dequant_word(wb_w[w], s2b);
+                const uint32_t kk = static_cast<uint32_t>(kr0 + i * kBlockK + 32 * t + 8 * w);
+                const int gr =
+                    min(static_cast<int>((static_cast<uint64_t>(kk) * p.g_magic) >> 32), p.ngroups - 1) - g_lo;
+                const uint4 qa = dequant_word(wa_w[w], __half2half2(scl[gr * 128 + ja]));
+                const uint4 qb = dequant_word(wb_w[w], __half2half2(scl[gr * 128 + ja + 8]));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint32_t afr[4] = {u ? qa.z : qa.x, u ? qb.z : qb.x, u ? qa.w : qa.y, u ? qb.w : qb.y};
@@ -376,7 +303,7 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
         issue_block(li + kDepth);  // this thread's slot for local block li is consumed (values decoded above)
     }
     cp_async_wait<0>();
-    if (GATED || !p.post_scale) {
+    if (!p.post_scale) {
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
 #pragma unroll
@@ -403,30 +330,9 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
         }
     }
 
-    if (LORA) grid_dependency_wait();  // V is complete (and the output may be written)
-    const int na = nt * kCols + ja;
-    // One gated output: H, and the projections if they are kept.
-    auto store_gated = [&](int m, int n, float gv, float uv) {
-        const int64_t o = static_cast<int64_t>(m) * p.N + n;
-        Cp[o] = __float2half_rn(gate_value(gv, p.act) * uv);
-        if (p.Pg) {
-            p.Pg[o] = __float2half_rn(gv);
-            p.Pu[o] = __float2half_rn(uv);
-        }
-    };
+    const int na = nt * 128 + ja;
     if (S == 1) {
         if (kh != 0) return;
-        if constexpr (GATED) {
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int m = 8 * j + 2 * t + e;
-                    if (m < Mrows && na < p.N) store_gated(m, na, acc[j][e], acc[j][2 + e]);
-                }
-            }
-            return;
-        }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             const int m0 = 8 * j + 2 * t;
@@ -434,7 +340,6 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
             for (int e = 0; e < 4; ++e) {
                 const int m = m0 + (e & 1);
                 const int n = na + ((e >> 1) << 3);
-                if (LORA && m < Mrows && n < p.N) acc[j][e] += lora_term(p.lora, p.N, m, n);
                 if (m < Mrows && n < p.N)
                     Cp[static_cast<int64_t>(m) * p.N + n] =
                         GROUPED ? epilogue_value(acc[j][e], p.act) : __float2half_rn(acc[j][e]);
@@ -456,34 +361,15 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int m = m0 + (e & 1);
-                // Row of the reduced tile: the weight column, or (gated) the gate-up
-                // pair of a column side by side, which one rank owns whole.
-                const int col = GATED ? 2 * ja + (e >> 1) : ja + ((e >> 1) << 3);
-                const int q = GATED ? (ja * S) >> 6 : (col * S) >> 7;  // owner of this column
-                const int cq = GATED ? 2 * ((q * 64 + S - 1) / S) : (q * 128 + S - 1) / S;  // owner's first row
+                const int col = ja + ((e >> 1) << 3);
+                const int q = (col * S) >> 7;          // owner of this column
+                const int cq = (q * 128 + S - 1) / S;  // owner's first column
                 if (m < Mrows)
                     st_dsmem_f32(&red[(rank * MP + m) * cwm + (col - cq)], static_cast<uint32_t>(q), acc[j][e]);
             }
         }
     }
     cluster_sync_all();
-    if constexpr (GATED) {
-        const int c0 = (rank * 64 + S - 1) / S, cw = ((rank + 1) * 64 + S - 1) / S - c0;
-        for (int o = threadIdx.x; o < cw * Mrows; o += kThreads) {
-            const int m = o / cw, c = o - m * cw;
-            const int n = nt * 64 + c0 + c;
-            if (n < p.N) {
-                float gv = 0.f, uv = 0.f;
-                for (int r = 0; r < S; ++r) {
-                    const float2 v = *reinterpret_cast<const float2*>(&red[(r * MP + m) * cwm + 2 * c]);
-                    gv += v.x;
-                    uv += v.y;
-                }
-                store_gated(m, n, gv, uv);
-            }
-        }
-        return;
-    }
     const int c0 = (rank * 128 + S - 1) / S, c1 = ((rank + 1) * 128 + S - 1) / S, cw = c1 - c0;
     for (int o = threadIdx.x; o < cw * Mrows; o += kThreads) {
         const int m = o / cw, c = o - m * cw;
@@ -491,7 +377,6 @@ __global__ void __launch_bounds__(KH * kSkThreads, 2)
         if (n < p.N) {
             float sum = 0.f;
             for (int r = 0; r < S; ++r) sum += red[(r * MP + m) * cwm + c];
-            if (LORA) sum += lora_term(p.lora, p.N, m, n);
             Cp[static_cast<int64_t>(m) * p.N + n] = GROUPED ? epilogue_value(sum, p.act) : __float2half_rn(sum);
         }
     }
@@ -527,7 +412,7 @@ int skinny_plan_fill(int64_t M, int64_t N, int64_t K, int64_t G, int splits, int
     const int64_t rows = krange / G + 2;
     const int64_t bytes =
         smem_bytes(kh, depth, mt, splits, static_cast<int>(stride), static_cast<int>(rows));
-    if (bytes > kMaxSmem) return W4A16_ERR_UNSUPPORTED;
+    if (bytes > 200 * 1024) return W4A16_ERR_UNSUPPORTED;
     // floor(k / G) as a multiply-shift over the padded K range. With
     // magic = (2^32 + e) / G, 0 <= e < G, k * magic / 2^32 = k / G + k * e / (G * 2^32),
     // which floors to floor(k / G) whenever k * e < 2^32 (the fractional part of
@@ -602,18 +487,6 @@ int skinny_plan_grouped(int64_t total_rows, int64_t N, int64_t K, int64_t G, Ski
     return W4A16_ERR_UNSUPPORTED;
 }
 
-int skinny_plan_gated(int64_t M, int64_t N, int64_t K, int64_t G, SkinnyPlan* plan) {
-    // A dense product of 2 N columns, but for the reduction buffer: a rank's
-    // slice is made of whole gate-up pairs.
-    const int rc = skinny_plan(M, 2 * N, K, G, plan);
-    if (rc) return rc;
-    if (plan->splits > 1) {
-        const int S = plan->splits;
-        plan->smem += S * 8 * plan->mt * 4 * (2 * ((64 + S - 1) / S) - (128 + S - 1) / S);
-    }
-    return plan->smem <= kMaxSmem ? W4A16_OK : W4A16_ERR_UNSUPPORTED;
-}
-
 int skinny_device_status(bool clear) {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_skinny_status, sizeof(int)) != cudaSuccess) return -1;
@@ -627,31 +500,24 @@ int skinny_device_status(bool clear) {
 namespace {
 
 // Launch with filled parameters; grid z = 1 (dense) or the number of experts.
-int skinny_launch_params(const SkinnyPlan& plan, SkinnyForm form, SkinnyParams& p, int64_t N, int64_t K, int64_t G,
-                         unsigned grid_z, cudaStream_t stream) {
-    constexpr int kForms = 24;
-    static bool attr_done[kForms][64] = {};
+int skinny_launch_params(const SkinnyPlan& plan, SkinnyParams& p, int64_t N, int64_t K, int64_t G, unsigned grid_z,
+                         cudaStream_t stream) {
+    static bool attr_done[12][64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
     const int kh = plan.threads / kSkThreads;
-    const int vi = 6 * form + (plan.mt == 2 ? 4 : (kh == 2 ? 2 : 0)) + (plan.depth == 8 / kh ? 1 : 0);
+    const int vi = (p.grouped ? 6 : 0) + (plan.mt == 2 ? 4 : (kh == 2 ? 2 : 0)) + (plan.depth == 8 / kh ? 1 : 0);
     // (shared-memory carve-out: the largest, so two CTAs fit per SM)
-    void (*kernels[kForms])(SkinnyParams) = {
-        w4a16_skinny_kernel<1, 4, 1, kDense>,   w4a16_skinny_kernel<1, 8, 1, kDense>,
-        w4a16_skinny_kernel<1, 2, 2, kDense>,   w4a16_skinny_kernel<1, 4, 2, kDense>,
-        w4a16_skinny_kernel<2, 4, 1, kDense>,   w4a16_skinny_kernel<2, 8, 1, kDense>,
-        w4a16_skinny_kernel<1, 4, 1, kGrouped>, w4a16_skinny_kernel<1, 8, 1, kGrouped>,
-        w4a16_skinny_kernel<1, 2, 2, kGrouped>, w4a16_skinny_kernel<1, 4, 2, kGrouped>,
-        w4a16_skinny_kernel<2, 4, 1, kGrouped>, w4a16_skinny_kernel<2, 8, 1, kGrouped>,
-        w4a16_skinny_kernel<1, 4, 1, kGated>,   w4a16_skinny_kernel<1, 8, 1, kGated>,
-        w4a16_skinny_kernel<1, 2, 2, kGated>,   w4a16_skinny_kernel<1, 4, 2, kGated>,
-        w4a16_skinny_kernel<2, 4, 1, kGated>,   w4a16_skinny_kernel<2, 8, 1, kGated>,
-        w4a16_skinny_kernel<1, 4, 1, kLora>,    w4a16_skinny_kernel<1, 8, 1, kLora>,
-        w4a16_skinny_kernel<1, 2, 2, kLora>,    w4a16_skinny_kernel<1, 4, 2, kLora>,
-        w4a16_skinny_kernel<2, 4, 1, kLora>,    w4a16_skinny_kernel<2, 8, 1, kLora>};
+    void (*kernels[12])(SkinnyParams) = {
+        w4a16_skinny_kernel<1, 4, 1, false>, w4a16_skinny_kernel<1, 8, 1, false>,
+        w4a16_skinny_kernel<1, 2, 2, false>, w4a16_skinny_kernel<1, 4, 2, false>,
+        w4a16_skinny_kernel<2, 4, 1, false>, w4a16_skinny_kernel<2, 8, 1, false>,
+        w4a16_skinny_kernel<1, 4, 1, true>,  w4a16_skinny_kernel<1, 8, 1, true>,
+        w4a16_skinny_kernel<1, 2, 2, true>,  w4a16_skinny_kernel<1, 4, 2, true>,
+        w4a16_skinny_kernel<2, 4, 1, true>,  w4a16_skinny_kernel<2, 8, 1, true>};
     if (!attr_done[vi][dev]) {
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess ||
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess ||
             cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
                                  cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
                 cudaSuccess)
@@ -705,7 +571,7 @@ int skinny_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt, cons
     p.C = reinterpret_cast<__half*>(C);
     p.M = static_cast<int32_t>(M);
     p.prefetch = static_weights_enabled() ? 1 : 0;
-    return skinny_launch_params(plan, kDense, p, N, K, G, 1, stream);
+    return skinny_launch_params(plan, p, N, K, G, 1, stream);
 }
 
 int skinny_grouped_launch(const SkinnyPlan& plan, const void* A, const uint8_t* const* Wt, const void* const* S,
@@ -722,43 +588,12 @@ int skinny_grouped_launch(const SkinnyPlan& plan, const void* A, const uint8_t* 
     p.A = reinterpret_cast<const __half*>(A);
     p.C = reinterpret_cast<__half*>(C);
     p.M = static_cast<int32_t>(total_rows);
+    p.grouped = 1;
     p.E = static_cast<int32_t>(E);
     p.act = act;
     p.offsets = offsets;
     p.prefetch = 0;  // the expert of a CTA is known only after the offsets, which follow the wait
-    return skinny_launch_params(plan, kGrouped, p, N, K, G, static_cast<unsigned>(E), stream);
-}
-
-int skinny_lora_launch(const SkinnyPlan& plan, const LoraOperands& lora, const void* A, const uint8_t* Wt,
-                       const void* S, void* C, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream) {
-    SkinnyParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.wt = Wt;
-    p.sc = reinterpret_cast<const __half*>(S);
-    p.A = reinterpret_cast<const __half*>(A);
-    p.C = reinterpret_cast<__half*>(C);
-    p.M = static_cast<int32_t>(M);
-    p.lora = lora;
-    return skinny_launch_params(plan, kLora, p, N, K, G, 1, stream);
-}
-
-int skinny_gated_launch(const SkinnyPlan& plan, const void* A, const uint8_t* Wt_gate, const void* S_gate,
-                        const uint8_t* Wt_up, const void* S_up, void* H, void* Pg, void* Pu, int64_t M, int64_t N,
-                        int64_t K, int64_t G, int act, cudaStream_t stream) {
-    SkinnyParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.wt = Wt_gate;
-    p.sc = reinterpret_cast<const __half*>(S_gate);
-    p.wt2 = Wt_up;
-    p.sc2 = reinterpret_cast<const __half*>(S_up);
-    p.A = reinterpret_cast<const __half*>(A);
-    p.C = reinterpret_cast<__half*>(H);
-    p.Pg = reinterpret_cast<__half*>(Pg);
-    p.Pu = reinterpret_cast<__half*>(Pu);
-    p.M = static_cast<int32_t>(M);
-    p.act = act;
-    p.prefetch = static_weights_enabled() ? 1 : 0;
-    return skinny_launch_params(plan, kGated, p, N, K, G, 1, stream);
+    return skinny_launch_params(plan, p, N, K, G, static_cast<unsigned>(E), stream);
 }
 
 }  // namespace w4a16
