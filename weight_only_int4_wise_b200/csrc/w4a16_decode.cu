@@ -69,7 +69,7 @@ struct DecodeParams {
     int32_t iters;            // blocks of a warp: ceil(KB / KS)
     int32_t piece;            // iterations whose activations are staged together (a multiple of kAhead)
     int32_t row_bytes;        // staged activation row
-    uint32_t g_magic;         // floor(k / G) == (k * g_magic) >> 32 (0: divide)
+    uint32_t g_magic;         // floor(k / G) == (k * g_magic) >> 32
     int32_t act, prefetch;
     LoraOperands lora;
 };
@@ -80,6 +80,17 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+
+// A scale: through L1, or past it (see the adapter form's early reads).
+template <bool PAST_L1>
+__device__ __forceinline__ uint16_t ld_scale(const void* p) {
+    uint16_t v;
+    if constexpr (PAST_L1)
+        asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    else
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 
@@ -104,36 +115,46 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
     const int nb = LORA ? na + 8 : na;
     float4* red = reinterpret_cast<float4*>(sm + p.M * p.row_bytes);
 
-    const int64_t chunk0 = static_cast<int64_t>(t >> 1) * 4096 + (t & 1) * 2048;
-    const uint8_t* wa = p.wt[0] + static_cast<int64_t>(na >> 7) * p.KT * 4096 + (na & 127) * 16 + chunk0;
-    const uint8_t* wb = p.wt[1] + static_cast<int64_t>(nb >> 7) * p.KT * 4096 + (nb & 127) * 16 + chunk0;
-    const __half* sa = p.sc[0] + na;
-    const __half* sb = p.sc[1] + (nb < p.N ? nb : 0);
-    const int kt_end = active ? p.KT - (t >> 1) : 0;  // block b has this chunk if 2b < kt_end
-
     struct Block {
         uint4 a, b;
-        __half sa[kNS], sb[kNS];
+        uint16_t sa[kNS], sb[kNS];
     };
-    auto load_scale = [](const __half* q) { return LORA ? __ldcg(q) : __ldg(q); };
-    auto load = [&](Block& x, int it) {
-        const int b = it * p.KS + kh;
-        if (2 * b < kt_end) {
-            const int64_t off = static_cast<int64_t>(b) * 8192;
+    // Running state of the loads, in 32 bits (the weights are below 4 GB): the next
+    // block's byte offset, the same for both rows but for a constant, its first k,
+    // and how many blocks are left. (The loads are volatile: left free, the compiler
+    // moves the scale loads down to their use and waits there for each of them.)
+    uint32_t w_off = static_cast<uint32_t>(((na >> 7) * static_cast<int64_t>(p.KT) + 2 * kh + (t >> 1)) * 4096 +
+                                           (t & 1) * 2048 + (na & 127) * 16);
+    const uint32_t w_step = static_cast<uint32_t>(p.KS) * 8192u;
+    uint32_t k_next = static_cast<uint32_t>(kh * kBlockK + 32 * t);
+    const uint32_t row_step = 2u * static_cast<uint32_t>(p.N);  // bytes of a scale row
+    const uint32_t s_off = 2u * static_cast<uint32_t>(na);
+    const uint32_t sb_more = LORA && nb < p.N ? 16u : 0u;       // (a row past N reads row g's scales; it is not written)
+    const uint8_t* wa = p.wt[0];
+    const uint8_t* wb = LORA ? wa + 128 : p.wt[1];
+    const uint8_t* sa = reinterpret_cast<const uint8_t*>(p.sc[0]);
+    const uint8_t* sb = LORA ? sa : reinterpret_cast<const uint8_t*>(p.sc[1]);
+    const int blocks = active && kh < p.KB ? (p.KB - kh + p.KS - 1) / p.KS : 0;  // this warp's
+    int to_load = blocks;
+    auto load = [&](Block& x) {
+        if (to_load > 0) {  // (the same for the whole warp)
+            --to_load;
+            // K may end in the middle of the last block: a chunk that does not exist
+            // reads the block's first tile, with scales of zero.
+            const bool missing = k_next >= static_cast<uint32_t>(p.KT) * 64u;
+            const uint32_t off = missing ? w_off - 4096u : w_off;
             x.a = ld_stream_v4(wa + off);
             x.b = ld_stream_v4(wb + off);
 #pragma unroll
             for (int q = 0; q < kNS; ++q) {
-                const uint32_t k = static_cast<uint32_t>(b * kBlockK + 32 * t + 16 * q);
-                const uint32_t gi = p.g_magic ? __umulhi(k, p.g_magic) : k / static_cast<uint32_t>(p.G);
-                const int64_t row = static_cast<int64_t>(min(static_cast<int>(gi), p.ngroups - 1)) * p.N;
-                x.sa[q] = load_scale(sa + row);
-                x.sb[q] = load_scale(sb + row);
+                const uint32_t gi = min(__umulhi(k_next + 16 * q, p.g_magic), static_cast<uint32_t>(p.ngroups - 1));
+                const uint32_t so = gi * row_step + s_off;
+                x.sa[q] = ld_scale<LORA>(sa + so);
+                x.sb[q] = ld_scale<LORA>(sb + (so + sb_more));
+                if (missing) x.sa[q] = x.sb[q] = 0;
             }
-        } else {
-            x.a = x.b = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int q = 0; q < kNS; ++q) x.sa[q] = x.sb[q] = __ushort_as_half(0);
+            w_off += w_step;
+            k_next += p.KS * kBlockK;
         }
     };
 
@@ -144,13 +165,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
     // at once, not through L1, and it waits for that kernel just before it reads V.)
     if (LORA || p.prefetch) {
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) load(blk[d], d);
+        for (int d = 0; d < kAhead; ++d) load(blk[d]);
     }
     grid_launch_dependents();
     if (!LORA) grid_dependency_wait();
     if (!LORA && !p.prefetch) {
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) load(blk[d], d);
+        for (int d = 0; d < kAhead; ++d) load(blk[d]);
     }
 
     float acc[2][MT][4];  // two chains: the even and the odd 16-deep steps
@@ -169,43 +190,46 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
             const int b0 = i0 * p.KS;
             const int units = (min(p.KB, b0 + p.piece * p.KS) - b0) * 16;  // 16-byte units per row
             if (i0 > 0) __syncthreads();  // the piece before is consumed
+            // (Asynchronous copies: all of a thread's 16-byte units are in flight at once.)
             for (int m = 0; m < p.M; ++m) {
                 const __half* src = p.A + static_cast<int64_t>(m) * p.K + b0 * kBlockK;
                 uint8_t* dst = sm + m * p.row_bytes;
                 for (int c = threadIdx.x; c < units; c += static_cast<int>(blockDim.x)) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (b0 * kBlockK + 8 * c < p.K) v = __ldcg(reinterpret_cast<const uint4*>(src + 8 * c));
-                    *reinterpret_cast<uint4*>(dst + (c >> 4) * 256 + ((c & 3) * 4 + ((c >> 2) & 3)) * 16) = v;
+                    const bool in = b0 * kBlockK + 8 * c < p.K;
+                    cp_async16(dst + (c >> 4) * 256 + ((c & 3) * 4 + ((c >> 2) & 3)) * 16, in ? src + 8 * c : p.A,
+                               in ? 16u : 0u);
                 }
             }
+            cp_async_commit();
+            cp_async_wait<0>();
             __syncthreads();
         }
         const int iend = min(p.iters, i0 + p.piece);
+        uint32_t off = static_cast<uint32_t>(kh) * 256;  // this warp's block in the staged piece
+        int left = min(iend, blocks) - i0;               // its blocks of the piece
         for (int i = i0; i < iend; i += kAhead) {
 #pragma unroll
             for (int d = 0; d < kAhead; ++d) {
-                if (i + d < iend) {
-                    Block& x = blk[d];
-                    const uint32_t off = static_cast<uint32_t>(((i + d - i0) * p.KS + kh) * 256);
-                    const bool have = active && (i + d) * p.KS + kh < p.KB;  // (the same for the whole warp)
+                Block& x = blk[d];
+                if (left > 0) {  // (the same for the whole warp)
                     const uint32_t aw[4] = {x.a.x, x.a.y, x.a.z, x.a.w};
                     const uint32_t bw[4] = {x.b.x, x.b.y, x.b.z, x.b.w};
-                    if (have) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint4 qa = dequant_word(aw[w], __half2half2(x.sa[FINE ? w >> 1 : 0]));
-                            const uint4 qb = dequant_word(bw[w], __half2half2(x.sb[FINE ? w >> 1 : 0]));
-                            const uint32_t f0[4] = {qa.x, qb.x, qa.y, qb.y};
-                            const uint32_t f1[4] = {qa.z, qb.z, qa.w, qb.w};
+                    for (int w = 0; w < 4; ++w) {
+                        const uint4 qa = dequant_word(aw[w], __half2half2(__ushort_as_half(x.sa[FINE ? w >> 1 : 0])));
+                        const uint4 qb = dequant_word(bw[w], __half2half2(__ushort_as_half(x.sb[FINE ? w >> 1 : 0])));
+                        const uint32_t f0[4] = {qa.x, qb.x, qa.y, qb.y};
+                        const uint32_t f1[4] = {qa.z, qb.z, qa.w, qb.w};
 #pragma unroll
-                            for (int j = 0; j < MT; ++j) {
-                                const uint4 y = lds128(arow[j] + off + 64 * w);
-                                mma_m16n8k16(acc[0][j], f0, y.x, y.y);
-                                mma_m16n8k16(acc[1][j], f1, y.z, y.w);
-                            }
+                        for (int j = 0; j < MT; ++j) {
+                            const uint4 y = lds128(arow[j] + off + 64 * w);
+                            mma_m16n8k16(acc[0][j], f0, y.x, y.y);
+                            mma_m16n8k16(acc[1][j], f1, y.z, y.w);
                         }
                     }
-                    load(x, i + d + kAhead);
+                    load(x);
+                    off += static_cast<uint32_t>(p.KS) * 256;
+                    --left;
                 }
             }
         }
@@ -311,6 +335,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
 
 // ====================================================================== host
 
+// floor(k / G) as a multiply-shift for every k < kend: with magic = (2^32 + e) / G,
+// 0 <= e < G, k * magic / 2^32 = k / G + k * e / (G * 2^32) floors to floor(k / G)
+// whenever k * e < 2^32 (the fractional part of k / G is at most (G - 1) / G). One
+// group needs no multiplier. False if some k might come out wrong (K above 2^32 / G).
+bool group_magic(int64_t G, int64_t kend, uint32_t* magic) {
+    *magic = 0;
+    if (G >= kend) return true;
+    const uint64_t g = static_cast<uint64_t>(G);
+    const uint64_t m = ((uint64_t(1) << 32) + g - 1) / g;
+    const uint64_t e = m * g - (uint64_t(1) << 32);
+    if (e != 0 && static_cast<uint64_t>(kend) > ((uint64_t(1) << 32) - 1) / e) return false;
+    *magic = static_cast<uint32_t>(m);
+    return true;
+}
+
 typedef void (*DecodeKernel)(DecodeParams);
 
 int decode_launch(DecodeParams& p, DecodeForm form, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream) {
@@ -359,7 +398,7 @@ int decode_launch(DecodeParams& p, DecodeForm form, int64_t M, int64_t N, int64_
     p.iters = (p.KB + p.KS - 1) / p.KS;
     p.piece = blocks >= p.KB ? (p.iters + kAhead - 1) / kAhead * kAhead : blocks / p.KS / kAhead * kAhead;
     p.row_bytes = std::min(p.piece * p.KS, p.KB) * 256 + 64;
-    p.g_magic = group_magic(G, static_cast<int64_t>(p.KB) * kBlockK);
+    if (!group_magic(G, static_cast<int64_t>(p.KB) * kBlockK, &p.g_magic)) return W4A16_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tiles + P - 1) / P), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(p.P * p.KS * 32), 1, 1);
@@ -375,16 +414,10 @@ int decode_launch(DecodeParams& p, DecodeForm form, int64_t M, int64_t N, int64_
 
 }  // namespace
 
-// floor(k / G) as a multiply-shift for every k < kend, k a multiple of 8: with
-// magic = (2^32 + e) / G, 0 <= e < G, k * magic / 2^32 = k / G + k * e / (G * 2^32)
-// floors to floor(k / G) whenever k * e < 2^32 (the fractional part of k / G is at
-// most (G - 1) / G). 0 if that does not hold for every k.
-uint32_t group_magic(int64_t G, int64_t kend) {
-    const uint64_t g = static_cast<uint64_t>(G);
-    const uint64_t magic = ((uint64_t(1) << 32) + g - 1) / g;
-    const uint64_t e = magic * g - (uint64_t(1) << 32);
-    if (magic > 0xFFFFFFFFull || (e != 0 && static_cast<uint64_t>(kend) > ((uint64_t(1) << 32) - 1) / e)) return 0;
-    return static_cast<uint32_t>(magic);
+bool decode_takes(int64_t M, int64_t N, int64_t K, int64_t G) {
+    uint32_t magic;
+    return M <= kSkinnyMaxM && w4a16_tiled_bytes(K, N) < (int64_t(1) << 32) &&
+           group_magic(G, (K + 127) / 128 * 128, &magic);
 }
 
 int decode_gated_launch(const void* A, const uint8_t* Wt_gate, const void* S_gate, const uint8_t* Wt_up,

@@ -1474,7 +1474,7 @@ namespace w4a16 {
 
 int lora_plan(int64_t M, int64_t N, int64_t K, int64_t G, LoraPlan* plan) {
     plan->tile_rows = 0;
-    if (M <= kSkinnyMaxM) return W4A16_OK;
+    if (decode_takes(M, N, K, G)) return W4A16_OK;
     Plan tc;
     const int rc = plan_dense(M, N, K, &tc, true, 0, 0, kLoraInt4);
     if (rc) return rc;
@@ -1520,7 +1520,7 @@ namespace {
 int gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate, const w4a16_half* S_gate, const uint8_t* Wt_up,
                const w4a16_half* S_up, w4a16_half* H_dev, w4a16_half* Pg_dev, w4a16_half* Pu_dev, int64_t M, int64_t N,
                int64_t K, int64_t G, int act, cudaStream_t stream) {
-    if (M <= kSkinnyMaxM)
+    if (decode_takes(M, N, K, G))
         return decode_gated_launch(A_dev, Wt_gate, S_gate, Wt_up, S_up, H_dev, Pg_dev, Pu_dev, M, N, K, G, act, stream);
     Plan plan;
     int rc = plan_dense(M, N, K, &plan, true, 0, 0, kGatedInt4);

@@ -124,9 +124,9 @@ int decode_gated_launch(const void* A, const uint8_t* Wt_gate, const void* S_gat
 int decode_lora_launch(const LoraOperands& lora, const void* A, const uint8_t* Wt, const void* S, void* C, int64_t M,
                        int64_t N, int64_t K, int64_t G, cudaStream_t stream);
 
-// The multiplier of floor(k / G) = (k * magic) >> 32 for every k < kend that is a
-// multiple of 8, or 0 if there is none.
-uint32_t group_magic(int64_t G, int64_t kend);
+// Whether they take the shape (a scale group's index must fit their multiply-shift,
+// the weights' offsets 32 bits); the tensor-core kernel takes any.
+bool decode_takes(int64_t M, int64_t N, int64_t K, int64_t G);
 
 // Grouped-expert form of the skinny kernel (grid z = expert) for at most 16
 // gathered rows in total (plan from skinny_plan_grouped): rows
