@@ -148,12 +148,14 @@ __device__ __forceinline__ bool warp_drain_phase(uint64_t* bar, uint32_t parity)
 }
 
 // Adapter form: the index of the first adapter stage (the ring is taken by whole
-// pairs of stages) and the number of adapter stages, which the first CTA of a
-// K split takes; V and the tile's list come from the kernel before this one.
+// pairs of stages), and this CTA's range of the tile's adapter stages, which the
+// CTAs of a K split share. V and the tile's list come from the kernel before.
 __device__ __forceinline__ int lora_first(int nst) { return (nst + 1) & ~1; }
-__device__ __forceinline__ int lora_stages(const Params& p, int split) {
+__device__ __forceinline__ void lora_range(const Params& p, int split, int* begin, int* count) {
     grid_dependency_wait();
-    return split == 0 ? (__ldcg(p.lora.count + blockIdx.z) * (p.lora.R / 8) + 7) / 8 : 0;
+    const int all = (__ldcg(p.lora.count + blockIdx.z) * (p.lora.R / 8) + 7) / 8;
+    *begin = split * all / p.splits;
+    *count = (split + 1) * all / p.splits - *begin;
 }
 
 // 0xFFFF in each half of x that holds an infinity or NaN (its exponent field is all ones).
@@ -413,7 +415,9 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
             }
             if constexpr (LORA) {
                 // The adapter stages, in the same ring from the next whole pair on.
-                const int first = lora_first(nst), end = first + lora_stages(p, split);
+                int begin, count;
+                lora_range(p, split, &begin, &count);
+                const int first = lora_first(nst), end = first + count;
                 for (int i = first; i < end && !stop; ++i) {
                     const int s = i % LS;
                     if ((i & 1) == 0 &&
@@ -494,33 +498,56 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         }
 
         if constexpr (LORA) {
-            const int first = lora_first(nst), end = first + lora_stages(p, split);
+            int begin, count;
+            lora_range(p, split, &begin, &count);
+            const int first = lora_first(nst), end = first + count;
             const int tid = static_cast<int>(threadIdx.x - 64) & (kGroupWarps * 32 - 1);  // inside the group
             const int32_t* list = p.lora.list + static_cast<int64_t>(blockIdx.z) * BN;
-            const int used = end > first ? __ldcg(p.lora.count + blockIdx.z) : 0;
+            const int used = __ldcg(p.lora.count + blockIdx.z);
             const int per = p.lora.R / 8;  // 8-rank chunks of one adapter
+            // The adapters of this thread's activation rows (tid, tid + 128).
+            constexpr int kRowsPer = (BN + kGroupWarps * 32 - 1) / (kGroupWarps * 32);
+            int row_id[kRowsPer];
+#pragma unroll
+            for (int x = 0; x < kRowsPer; ++x) {
+                const int row = tid + x * kGroupWarps * 32;
+                row_id[x] = row < rows ? __ldcg(p.lora.ids + m0 + row) : -1;
+            }
             int i = first + ((grp - first) % DQ + DQ) % DQ;
             for (; i < end; i += DQ) {
                 const int s = i % LS;
-                const int q0 = (i - first) * 8;  // chunk q of the stage: ranks 8 ((q0 + q) % per) of adapter (q0 + q) / per
-                uint32_t v[2][16];
-                uint32_t bad = 0;
+                // Chunk q of the stage holds ranks 8 rr .. + 7 of the d-th adapter of the
+                // list, (d, rr) = divmod(q0 + q, per). All loads of a kind go out together.
+                const int q0 = (begin + i - first) * 8;
+                int who[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const int d = (q0 + q) / per, rr = (q0 + q) - d * per;
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (d < used && col_ok)
-                        x = __ldcg(reinterpret_cast<const uint4*>(
-                            p.lora.LB + (static_cast<int64_t>(__ldcg(list + d)) * p.N + n) * p.lora.R + 8 * rr));
-                    // An infinity or NaN would meet the zeros of rows that do not use
-                    // this adapter: it is left out here, and its own rows get it in
-                    // the epilogue.
-                    uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                    const int d = (q0 + q) / per;
+                    who[q] = d < used ? __ldcg(list + d) : -1;
+                }
+                uint32_t v[2][16];
+                uint32_t bad = 0;
+                {
+                    uint4 x[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t m = nonfinite_halves(xs[e]);
-                        bad |= m;
-                        v[q >> 2][4 * (q & 3) + e] = xs[e] & ~m;
+                    for (int q = 0; q < 8; ++q) {
+                        x[q] = make_uint4(0u, 0u, 0u, 0u);
+                        if (who[q] >= 0 && col_ok)
+                            x[q] = __ldcg(reinterpret_cast<const uint4*>(
+                                p.lora.LB + (static_cast<int64_t>(who[q]) * p.N + n) * p.lora.R + (q0 + q) % per * 8));
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        // An infinity or NaN would meet the zeros of rows that do not use
+                        // this adapter: it is left out here, and its own rows get it in
+                        // the epilogue.
+                        const uint32_t xs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t m = nonfinite_halves(xs[e]);
+                            bad |= m;
+                            v[q >> 2][4 * (q & 3) + e] = xs[e] & ~m;
+                        }
                     }
                 }
                 if (bad) tile_info[5] = 1;
@@ -530,19 +557,21 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
                 tc_fence_after_sync();
                 tmem_st_32x32b_x16(tmem_ring + tlane + s * kSlotCols, v[0]);
                 tmem_st_32x32b_x16(tmem_ring + tlane + s * kSlotCols + 16, v[1]);
-                for (int row = tid; row < BN; row += kGroupWarps * 32) {
-                    const int id = row < rows ? __ldcg(p.lora.ids + m0 + row) : -1;
+#pragma unroll
+                for (int x = 0; x < kRowsPer; ++x) {
+                    const int row = tid + x * kGroupWarps * 32;
+                    if (row >= BN) break;
                     const uint32_t dst = smem_addr(smem + L::kAct + s * L::kActBytes) + row * 128;
+                    const __half* vrow = p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R;
+                    uint4 y[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        const int d = (q0 + q) / per, rr = (q0 + q) - d * per;
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (d < used && id >= 0 && __ldcg(list + d) == id) {
-                            x = __ldcg(reinterpret_cast<const uint4*>(
-                                p.lora.V + static_cast<int64_t>(m0 + row) * p.lora.R + 8 * rr));
-                        }
-                        sts128(dst + ((q ^ (row & 7)) << 4), x);
+                        y[q] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row_id[x] >= 0 && who[q] == row_id[x])
+                            y[q] = __ldcg(reinterpret_cast<const uint4*>(vrow + (q0 + q) % per * 8));
                     }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) sts128(dst + ((q ^ (row & 7)) << 4), y[q]);
                 }
                 fence_proxy_async_smem();
                 tmem_st_wait();
@@ -564,6 +593,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
         // adapter's terms that the MMA left out.
         const bool fix = LORA && have_acc && *(volatile int*)&tile_info[5] != 0;
         auto lora_fix = [&](uint32_t (&v)[16], int c) {
+#pragma unroll  // (v stays in registers)
             for (int t = 0; t < 16; ++t) {
                 const int row = c * 16 + t;
                 const int id = row < rows && col_ok ? __ldcg(p.lora.ids + m0 + row) : -1;

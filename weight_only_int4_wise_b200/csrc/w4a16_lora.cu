@@ -67,27 +67,40 @@ __device__ __forceinline__ int adapter_of(const DownParams& p, int m) {
     return id;
 }
 
-// The distinct adapters of token tile z, in the order of their first rows.
-__device__ void list_adapters(const DownParams& p, int z, int* sid, int* wcount) {
+// The distinct adapters of token tile z (at most 256 rows), in the order of their
+// first rows: each warp's own by a match over its lanes, then, for those only,
+// against the lists of the warps before it.
+__device__ void list_adapters(const DownParams& p, int z, int* lists /* [8][32] */, int* counts /* [2][8] */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool mine = tid < 256;
     const int id = tid < p.tile_rows ? adapter_of(p, z * p.tile_rows + tid) : -1;
-    sid[tid] = id;
-    __syncthreads();
-    bool first = id >= 0;
-    for (int i = 0; i < tid; i += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(sid + i);
-        first = first && !((v.x == id) | (v.y == id && i + 1 < tid) | (v.z == id && i + 2 < tid) |
-                           (v.w == id && i + 3 < tid));
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    bool first = id >= 0 && (same & ((1u << lane) - 1u)) == 0;
+    uint32_t b = __ballot_sync(0xffffffffu, first);
+    if (mine) {
+        lists[warp * 32 + lane] = -1;
+        __syncwarp();
+        if (first) lists[warp * 32 + __popc(b & ((1u << lane) - 1u))] = id;
+        if (lane == 0) counts[warp] = __popc(b);
     }
-    const uint32_t b = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) wcount[warp] = __popc(b);
     __syncthreads();
+    if (mine && b) {
+        for (int w = 0; w < warp; ++w)
+            for (int i = 0; i < counts[w]; i += 4) {  // (padded with -1)
+                const int4 v = *reinterpret_cast<const int4*>(lists + w * 32 + i);
+                first = first && v.x != id && v.y != id && v.z != id && v.w != id;
+            }
+    }
+    b = __ballot_sync(0xffffffffu, first);
+    if (mine && lane == 0) counts[8 + warp] = __popc(b);
+    __syncthreads();
+    if (!mine) return;
     int at = __popc(b & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) at += wcount[w];
+    for (int w = 0; w < warp; ++w) at += counts[8 + w];
     if (first) p.list[static_cast<int64_t>(z) * p.tile_rows + at] = id;
     if (tid == 0) {
         int n = 0;
-        for (int w = 0; w < kWarps; ++w) n += wcount[w];
+        for (int w = 0; w < 8; ++w) n += counts[8 + w];
         p.count[z] = n;
     }
 }
@@ -95,13 +108,13 @@ __device__ void list_adapters(const DownParams& p, int z, int* sid, int* wcount)
 template <int RT>
 __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p) {
     __shared__ __align__(16) float red[kWarps * kRows * 8 * RT];
+    __shared__ int group_ids[kRows];
     grid_dependency_wait();    // the operands may come from the previous kernel
     __threadfence();
     grid_launch_dependents();  // (only now: the product's early loads rely on that kernel being complete)
     if (static_cast<int>(blockIdx.x) >= p.groups) {
         if (blockIdx.y == 0 && blockIdx.z == 0)
-            list_adapters(p, blockIdx.x - p.groups, reinterpret_cast<int*>(red),
-                          reinterpret_cast<int*>(red) + kThreads);
+            list_adapters(p, blockIdx.x - p.groups, reinterpret_cast<int*>(red), reinterpret_cast<int*>(red) + 256);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -109,11 +122,14 @@ __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p)
     const int r0 = blockIdx.z * 8 * RT;
     // Distinct adapters of the group: the lowest lane of each set of equal rows.
     const int mine = lane < kRows ? adapter_of(p, m0 + lane) : -1;
+    const float my_scale = mine >= 0 && p.scaling ? p.scaling[mine] : 1.f;
+    if (warp == 0 && lane < kRows) group_ids[lane] = mine;  // (read after the first barrier below)
     const uint32_t same = __match_any_sync(0xffffffffu, mine);
     uint32_t leaders = __ballot_sync(0xffffffffu, mine >= 0 && (same & ((1u << lane) - 1u)) == 0);
     for (int slot = 0; leaders; ++slot, leaders &= leaders - 1) {
         if (slot % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
         const int id = __shfl_sync(0xffffffffu, mine, __ffs(leaders) - 1);
+        const float s = __shfl_sync(0xffffffffu, my_scale, __ffs(leaders) - 1);
         float acc[RT][4];
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
@@ -121,21 +137,30 @@ __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p)
         const __half* a1 = a0 + static_cast<int64_t>(8) * p.K;
         const bool ok0 = m0 + g < p.M, ok1 = m0 + g + 8 < p.M;
         const __half* lb = p.LA + (static_cast<int64_t>(id) * p.R + r0 + g) * p.K + 8 * t;
-#pragma unroll 4
-        for (int k = 32 * warp; k < p.K; k += 32 * kWarps) {
-            const bool in = k + 8 * t < p.K;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            const uint4 x0 = in && ok0 ? *reinterpret_cast<const uint4*>(a0 + k) : zero;
-            const uint4 x1 = in && ok1 ? *reinterpret_cast<const uint4*>(a1 + k) : zero;
-            const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y};
-            const uint32_t f1[4] = {x0.z, x1.z, x0.w, x1.w};
+        // Batches of blocks: all loads of a batch are issued before its first MMA.
+        constexpr int kBatch = RT == 4 ? 2 : 4;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int k0 = 32 * warp; k0 < p.K; k0 += 32 * kWarps * kBatch) {
+            uint4 x0[kBatch], x1[kBatch], y[kBatch][RT];
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                const uint4 y = in && r0 + 8 * j + g < p.R
-                                    ? ld_nc_v4(lb + static_cast<int64_t>(8 * j) * p.K + k)
-                                    : zero;
-                mma_m16n8k16(acc[j], f0, y.x, y.y);
-                mma_m16n8k16(acc[j], f1, y.z, y.w);
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + 32 * kWarps * u;
+                const bool in = k + 8 * t < p.K;
+                x0[u] = in && ok0 ? ld_nc_v4(a0 + k) : zero;
+                x1[u] = in && ok1 ? ld_nc_v4(a1 + k) : zero;
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+                    y[u][j] = in && r0 + 8 * j + g < p.R ? ld_nc_v4(lb + static_cast<int64_t>(8 * j) * p.K + k) : zero;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t f0[4] = {x0[u].x, x1[u].x, x0[u].y, x1[u].y};
+                const uint32_t f1[4] = {x0[u].z, x1[u].z, x0[u].w, x1[u].w};
+#pragma unroll
+                for (int j = 0; j < RT; ++j) {
+                    mma_m16n8k16(acc[j], f0, y[u][j].x, y[u][j].y);
+                    mma_m16n8k16(acc[j], f1, y[u][j].z, y[u][j].w);
+                }
             }
         }
 #pragma unroll
@@ -145,13 +170,12 @@ __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p)
             *reinterpret_cast<float2*>(d + 8 * 8 * RT) = make_float2(acc[j][2], acc[j][3]);
         }
         __syncthreads();
-        const float s = p.scaling ? p.scaling[id] : 1.f;
         for (int o = threadIdx.x; o < kRows * 8 * RT; o += kThreads) {
             const int m = m0 + o / (8 * RT), r = r0 + o % (8 * RT);
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) sum += red[w * kRows * 8 * RT + o];  // warp order
-            if (m < p.M && r < p.R && p.ids[m] == id) 
+            if (m < p.M && r < p.R && group_ids[m - m0] == id) 
                 p.V[static_cast<int64_t>(m) * p.R + r] = __float2half_rn(s * sum);
         }
         __syncthreads();
@@ -182,9 +206,9 @@ int lora_down(DownParams& p, int tiles, cudaStream_t stream) {
     // keep 16 or 32 together, so that A is read once per 16 or 32 ranks.
     const int rt = p.groups <= 8 ? 1 : (p.R <= 16 ? 2 : 4);
     const int chunks = (p.R + 8 * rt - 1) / (8 * rt);
-    // Adapters of a group side by side while the grid is below two CTAs per SM.
+    // Adapters of a group side by side while that leaves one CTA per SM.
     const int sms = sm_count() > 0 ? sm_count() : 148;
-    const int slots = std::max(1, std::min({kRows, static_cast<int>(p.M), 2 * sms / (p.groups * chunks)}));
+    const int slots = std::max(1, std::min({kRows, static_cast<int>(p.M), sms / (p.groups * chunks)}));
     const dim3 grid(static_cast<unsigned>(p.groups + tiles), static_cast<unsigned>(slots),
                     static_cast<unsigned>(chunks));
     switch (rt) {
