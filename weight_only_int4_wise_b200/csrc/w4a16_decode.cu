@@ -365,7 +365,10 @@ int decode_launch(DecodeParams& p, DecodeForm form, int64_t M, int64_t N, int64_
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
     if (!attr_done[vi][dev]) {
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
+                                 cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+                cudaSuccess)
             return W4A16_ERR_CUDA;
         attr_done[vi][dev] = true;
     }

@@ -491,6 +491,12 @@ int prepare_dgrad_device() {
                 cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared) != cudaSuccess)
                 return W4A16_ERR_CUDA;
+    // (The slopes kernel runs in front of the product: with the same carve-out the SMs
+    // need not drain in between.)
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(&gated_slopes_kernel),
+                             cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+        cudaSuccess)
+        return W4A16_ERR_CUDA;
     done[dev] = true;
     return W4A16_OK;
 }
@@ -542,6 +548,8 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
 
 int gated_slopes(const w4a16_half* dH, const w4a16_half* Pg, const w4a16_half* Pu, w4a16_half* dPg, w4a16_half* dPu,
                  int64_t elements, int act, cudaStream_t stream) {
+    const int rc = prepare_dgrad_device();
+    if (rc) return rc;
     const int64_t vecs = elements / 8;
     const int64_t cap = static_cast<int64_t>(sm_count() > 0 ? sm_count() : 148) * 8;
     const int64_t blocks = std::min<int64_t>(cap, (vecs + kSlopeThreads - 1) / kSlopeThreads);

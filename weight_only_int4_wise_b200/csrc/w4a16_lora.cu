@@ -16,7 +16,7 @@
 // for this kernel only where it reads V.
 //
 // down kernel: one CTA takes 16 rows, 8 * RT ranks and one distinct adapter of
-// those rows at a time (grid y strides over them); its 16 warps split K into
+// those rows at a time (grid y strides over them); its 16 (or 4) warps split K into
 // 32-deep blocks, read both operands straight from global memory into MMA
 // fragments (16 bytes per lane: inside a block the order of k is free as long
 // as both operands use it), and add their fp32 partials in warp order through
@@ -40,8 +40,6 @@ namespace {
 
 __device__ int g_lora_status;  // latched device-side error (0 = none)
 
-constexpr int kWarps = 16;
-constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;
 
 struct DownParams {
@@ -70,43 +68,65 @@ __device__ __forceinline__ int adapter_of(const DownParams& p, int m) {
 // The distinct adapters of token tile z (at most 256 rows), in the order of their
 // first rows: each warp's own by a match over its lanes, then, for those only,
 // against the lists of the warps before it.
+template <int W>
 __device__ void list_adapters(const DownParams& p, int z, int* lists /* [8][32] */, int* counts /* [2][8] */) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool mine = tid < 256;
-    const int id = tid < p.tile_rows ? adapter_of(p, z * p.tile_rows + tid) : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    bool first = id >= 0 && (same & ((1u << lane) - 1u)) == 0;
-    uint32_t b = __ballot_sync(0xffffffffu, first);
-    if (mine) {
-        lists[warp * 32 + lane] = -1;
-        __syncwarp();
-        if (first) lists[warp * 32 + __popc(b & ((1u << lane) - 1u))] = id;
-        if (lane == 0) counts[warp] = __popc(b);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kPer = W >= 8 ? 1 : 8 / W;  // 32-row sets of a warp: warp, warp + W, ...
+    int id[kPer];
+    uint32_t b[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        const int w = warp + x * W, r = w * 32 + lane;
+        id[x] = w < 8 && r < p.tile_rows ? adapter_of(p, z * p.tile_rows + r) : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, id[x]);
+        const bool first = id[x] >= 0 && (same & ((1u << lane) - 1u)) == 0;
+        b[x] = __ballot_sync(0xffffffffu, first);
+        if (w < 8) {
+            lists[w * 32 + lane] = -1;
+            __syncwarp();
+            if (first) lists[w * 32 + __popc(b[x] & ((1u << lane) - 1u))] = id[x];
+            if (lane == 0) counts[w] = __popc(b[x]);
+        }
     }
     __syncthreads();
-    if (mine && b) {
-        for (int w = 0; w < warp; ++w)
-            for (int i = 0; i < counts[w]; i += 4) {  // (padded with -1)
-                const int4 v = *reinterpret_cast<const int4*>(lists + w * 32 + i);
-                first = first && v.x != id && v.y != id && v.z != id && v.w != id;
-            }
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        const int w = warp + x * W;
+        bool first = (b[x] >> lane) & 1u;
+        if (w < 8 && b[x]) {
+            for (int v = 0; v < w; ++v)
+                for (int i = 0; i < counts[v]; i += 4) {  // (padded with -1)
+                    const int4 l = *reinterpret_cast<const int4*>(lists + v * 32 + i);
+                    first = first && l.x != id[x] && l.y != id[x] && l.z != id[x] && l.w != id[x];
+                }
+        }
+        b[x] = __ballot_sync(0xffffffffu, first);
+        if (w < 8 && lane == 0) counts[8 + w] = __popc(b[x]);
     }
-    b = __ballot_sync(0xffffffffu, first);
-    if (mine && lane == 0) counts[8 + warp] = __popc(b);
     __syncthreads();
-    if (!mine) return;
-    int at = __popc(b & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) at += counts[8 + w];
-    if (first) p.list[static_cast<int64_t>(z) * p.tile_rows + at] = id;
-    if (tid == 0) {
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        const int w = warp + x * W;
+        if (w >= 8) continue;
+        int at = __popc(b[x] & ((1u << lane) - 1u));
+        for (int v = 0; v < w; ++v) at += counts[8 + v];
+        if ((b[x] >> lane) & 1u) p.list[static_cast<int64_t>(z) * p.tile_rows + at] = id[x];
+    }
+    if (threadIdx.x == 0) {
         int n = 0;
-        for (int w = 0; w < 8; ++w) n += counts[8 + w];
+        for (int v = 0; v < 8; ++v) n += counts[8 + v];
         p.count[z] = n;
     }
 }
 
-template <int RT>
-__global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p) {
+// W = 16 warps where this kernel's latency counts. With many row groups W = 4: a CTA
+// of 128 threads and 8 K registers fits on an SM beside the product's CTA (576
+// threads, 55 K registers), so the product's K loop, which needs no V, runs at the
+// same time. (Both ask for the largest shared-memory carve-out: an SM changes it
+// only when it is empty.)
+template <int RT, int W>
+__global__ void __launch_bounds__(W * 32) lora_down_kernel(const DownParams p) {
+    constexpr int kWarps = W, kThreads = W * 32;
     __shared__ __align__(16) float red[kWarps * kRows * 8 * RT];
     __shared__ int group_ids[kRows];
     grid_dependency_wait();    // the operands may come from the previous kernel
@@ -114,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p)
     grid_launch_dependents();  // (only now: the product's early loads rely on that kernel being complete)
     if (static_cast<int>(blockIdx.x) >= p.groups) {
         if (blockIdx.y == 0 && blockIdx.z == 0)
-            list_adapters(p, blockIdx.x - p.groups, reinterpret_cast<int*>(red), reinterpret_cast<int*>(red) + 256);
+            list_adapters<W>(p, blockIdx.x - p.groups, reinterpret_cast<int*>(red), reinterpret_cast<int*>(red) + 256);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -133,27 +153,42 @@ __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p)
         float acc[RT][4];
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-        const __half* a0 = p.A + static_cast<int64_t>(m0 + g) * p.K + 8 * t;
-        const __half* a1 = a0 + static_cast<int64_t>(8) * p.K;
-        const bool ok0 = m0 + g < p.M, ok1 = m0 + g + 8 < p.M;
-        const __half* lb = p.LA + (static_cast<int64_t>(id) * p.R + r0 + g) * p.K + 8 * t;
+        // Rows past M and ranks past R read a row that exists; their sums are not
+        // written. (No load is conditional: a branch around a load would wait for
+        // its value where the two paths meet.)
+        const __half* a0 = p.A + static_cast<int64_t>(min(m0 + g, p.M - 1)) * p.K + 8 * t;
+        const __half* a1 = p.A + static_cast<int64_t>(min(m0 + g + 8, p.M - 1)) * p.K + 8 * t;
+        const __half* lb[RT];
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+            lb[j] = p.LA + (static_cast<int64_t>(id) * p.R + min(r0 + 8 * j + g, p.R - 1)) * p.K + 8 * t;
         // Batches of blocks: all loads of a batch are issued before its first MMA.
-        constexpr int kBatch = RT == 4 ? 2 : 4;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        // Chunks past K read the row's first one and are taken as zeros.
+        constexpr int kBatch = RT == 4 ? 2 : (RT == 2 ? 4 : 8);
         for (int k0 = 32 * warp; k0 < p.K; k0 += 32 * kWarps * kBatch) {
             uint4 x0[kBatch], x1[kBatch], y[kBatch][RT];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const int k = k0 + 32 * kWarps * u;
-                const bool in = k + 8 * t < p.K;
-                x0[u] = in && ok0 ? ld_nc_v4(a0 + k) : zero;
-                x1[u] = in && ok1 ? ld_nc_v4(a1 + k) : zero;
+                const int kk = k + 8 * t < p.K ? k : -8 * t;
+                x0[u] = ld_nc_v4(a0 + kk);
+                x1[u] = ld_nc_v4(a1 + kk);
 #pragma unroll
-                for (int j = 0; j < RT; ++j)
-                    y[u][j] = in && r0 + 8 * j + g < p.R ? ld_nc_v4(lb + static_cast<int64_t>(8 * j) * p.K + k) : zero;
+                for (int j = 0; j < RT; ++j) y[u][j] = ld_nc_v4(lb[j] + kk);
             }
+            __syncwarp();  // (keeps the loads together: the compiler would move each down to its MMA)
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
+                if (k0 + 32 * kWarps * u + 32 > p.K) {  // (the same for the whole warp)
+                    const uint32_t keep = k0 + 32 * kWarps * u + 8 * t < p.K ? 0xFFFFFFFFu : 0u;
+                    auto mask = [&](uint4& v) {
+                        v = make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep);
+                    };
+                    mask(x0[u]);
+                    mask(x1[u]);
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) mask(y[u][j]);
+                }
                 const uint32_t f0[4] = {x0[u].x, x1[u].x, x0[u].y, x1[u].y};
                 const uint32_t f1[4] = {x0[u].z, x1[u].z, x0[u].w, x1[u].w};
 #pragma unroll
@@ -182,39 +217,56 @@ __global__ void __launch_bounds__(kThreads) lora_down_kernel(const DownParams p)
     }
 }
 
+// Row groups from which the product's K loop hides the slower, narrow form.
+constexpr int kOverlapGroups = 64;
+
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
 
-template <int RT>
+template <int RT, int W>
 int launch_down(const DownParams& p, dim3 grid, cudaStream_t stream) {
+    static bool attr_done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
+    if (!attr_done[dev]) {
+        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(&lora_down_kernel<RT, W>),
+                                 cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+            return W4A16_ERR_CUDA;
+        attr_done[dev] = true;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(W * 32, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_down_kernel<RT>, p) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, lora_down_kernel<RT, W>, p) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
 }
 
 int lora_down(DownParams& p, int tiles, cudaStream_t stream) {
     p.groups = (p.M + kRows - 1) / kRows;
     // Ranks per CTA: few row groups spread the ranks over CTAs (8 each); many
     // keep 16 or 32 together, so that A is read once per 16 or 32 ranks.
-    const int rt = p.groups <= 8 ? 1 : (p.R <= 16 ? 2 : 4);
+    // (The narrow form has registers for 16.)
+    const bool narrow = p.groups >= kOverlapGroups;
+    const int rt = p.groups <= 8 ? 1 : (p.R <= 16 || narrow ? 2 : 4);
     const int chunks = (p.R + 8 * rt - 1) / (8 * rt);
-    // Adapters of a group side by side while that leaves one CTA per SM.
+    // Adapters of a group side by side while that leaves one CTA per SM, and always
+    // two: a group where one prompt ends and the next begins would take twice as long.
     const int sms = sm_count() > 0 ? sm_count() : 148;
-    const int slots = std::max(1, std::min({kRows, static_cast<int>(p.M), sms / (p.groups * chunks)}));
+    const int slots = std::min({kRows, static_cast<int>(p.M), std::max(2, sms / (p.groups * chunks))});
     const dim3 grid(static_cast<unsigned>(p.groups + tiles), static_cast<unsigned>(slots),
                     static_cast<unsigned>(chunks));
+    if (narrow) return launch_down<2, 4>(p, grid, stream);
     switch (rt) {
-        case 1: return launch_down<1>(p, grid, stream);
-        case 2: return launch_down<2>(p, grid, stream);
-        default: return launch_down<4>(p, grid, stream);
+        case 1: return launch_down<1, 16>(p, grid, stream);
+        case 2: return launch_down<2, 16>(p, grid, stream);
+        default: return launch_down<4, 16>(p, grid, stream);
     }
 }
 
