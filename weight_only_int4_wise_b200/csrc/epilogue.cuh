@@ -36,34 +36,50 @@ __device__ __forceinline__ __half epilogue_value(float acc, int act) {
 // As above, no form subtracts numbers near one: the normal CDF is erfc(-x / sqrt 2) / 2 and
 // both the tanh GELU and SiLU are x * t with t = 1 / (1 + e^(-z)), z = 2 sqrt(2/pi) (x + 0.044715 x^3)
 // or z = x, whose derivative is t + x t (1 - t) z'.
+// The logistic t uses the hardware exponential and division: where the result is
+// not below fp16's range (|z| < 30) their relative error is below 2^-18, against
+// the 2^-11 of its one rounding to fp16, and they take 6 instead of about 25
+// instructions (the gated epilogue at 2048 x 14336: 482 -> 465 us).
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
+__device__ __forceinline__ float logistic(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
 __device__ __forceinline__ float gate_value(float x, int act) {
     switch (act) {
-        case W4A16_ACT_SILU: return x / (1.f + expf(-x));
+        case W4A16_ACT_SILU: return x * logistic(x);
         case W4A16_ACT_GELU_ERF: return 0.5f * x * erfcf(x * -kSqrtHalf);
-        case W4A16_ACT_GELU_TANH: return x / (1.f + expf(-kTanhScale * (x + 0.044715f * x * x * x)));
+        case W4A16_ACT_GELU_TANH: return x * logistic(kTanhScale * (x + 0.044715f * x * x * x));
         case W4A16_ACT_RELU: return fmaxf(x, 0.f);
         default: return x;
     }
 }
 
-__device__ __forceinline__ float gate_slope(float x, int act) {
+// The derivative, and the value in *v.
+__device__ __forceinline__ float gate_slope(float x, int act, float* v) {
     switch (act) {
         case W4A16_ACT_SILU: {
-            const float t = 1.f / (1.f + expf(-x));
+            const float t = logistic(x);
+            *v = x * t;
             return fmaf(x * t, 1.f - t, t);
         }
-        case W4A16_ACT_GELU_ERF:
-            return fmaf(x * kInvSqrt2Pi, expf(-0.5f * x * x), 0.5f * erfcf(x * -kSqrtHalf));
+        case W4A16_ACT_GELU_ERF: {
+            const float t = 0.5f * erfcf(x * -kSqrtHalf);
+            *v = x * t;
+            return fmaf(x * kInvSqrt2Pi, __expf(-0.5f * x * x), t);
+        }
         case W4A16_ACT_GELU_TANH: {
-            const float t = 1.f / (1.f + expf(-kTanhScale * (x + 0.044715f * x * x * x)));
+            const float t = logistic(kTanhScale * (x + 0.044715f * x * x * x));
+            *v = x * t;
             return fmaf(x * t * (1.f - t), kTanhScale * (1.f + 0.134145f * x * x), t);
         }
-        case W4A16_ACT_RELU: return x > 0.f ? 1.f : 0.f;
-        default: return 1.f;
+        case W4A16_ACT_RELU:
+            *v = fmaxf(x, 0.f);
+            return x > 0.f ? 1.f : 0.f;
+        default:
+            *v = x;
+            return 1.f;
     }
 }
 

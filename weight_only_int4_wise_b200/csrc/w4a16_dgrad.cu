@@ -420,8 +420,10 @@ __global__ void __launch_bounds__(kSlopeThreads)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 h = __half22float2(h2[e]), a = __half22float2(g2[e]), b = __half22float2(u2[e]);
-            og2[e] = __floats2half2_rn(h.x * b.x * gate_slope(a.x, act), h.y * b.y * gate_slope(a.y, act));
-            ou2[e] = __floats2half2_rn(h.x * gate_value(a.x, act), h.y * gate_value(a.y, act));
+            float vx, vy;
+            const float dx = gate_slope(a.x, act, &vx), dy = gate_slope(a.y, act, &vy);
+            og2[e] = __floats2half2_rn(h.x * b.x * dx, h.y * b.y * dy);
+            ou2[e] = __floats2half2_rn(h.x * vx, h.y * vy);
         }
         reinterpret_cast<uint4*>(dG)[i] = og;
         reinterpret_cast<uint4*>(dU)[i] = ou;
