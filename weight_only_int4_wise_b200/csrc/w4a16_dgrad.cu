@@ -28,6 +28,11 @@
 //               16-byte row stores).
 // The two rings are separate because their costs are: a gradient tile (BN x 128
 // bytes) needs time to arrive, a decoded tile (16 KB) is made on the spot.
+// What bounds it is shared memory: per stage the decoded tile is written and read
+// (2 x 16 KB), the gradient tile too (2 x 32 KB at 256 rows), 768 cycles at 128
+// bytes per clock for 512 cycles of MMAs (measured: 800). So where the grid stays
+// full enough a CTA takes KM = 2 neighbouring blocks of 128 k (both accumulators fill
+// TMEM): the gradient tile is brought in once for both, 1280 cycles for 1024.
 // Few tiles split the contraction over a cluster of up to 8 CTAs; the fp32
 // partial tiles are summed in rank order (deterministic).
 #include <cuda.h>
@@ -66,6 +71,7 @@ struct DgradParams {
     const __half* sc[2];    // scales [ceil(K/G), N]
     __half* out;            // dA [rows, K]
     int32_t rows, N, K, G;
+    int32_t tile_rows;      // gradient rows per CTA (a multiple of 16 up to BN)
     int32_t ngroups, KT;    // ceil(K/G), ceil(K/64)
     int32_t NS;             // stages of one source: ceil(N/64)
     int32_t stages;         // all stages: sources * NS
@@ -76,20 +82,21 @@ struct DgradParams {
     int32_t stall_stage;    // test aid: withhold this stage's ready signal (< 0: never)
 };
 
-template <int BN, int LB, int LA>
+template <int BN, int LB, int LA, int KM>
 struct DgradLayout {
     static constexpr int kBBytes = BN * kDepth * 2;
+    static constexpr int kSlotA = KM * kABytes;  // the decoded tiles of one stage
     static constexpr int kB = 0;
     static constexpr int kA = kB + LB * kBBytes;
-    static constexpr int kBar = kA + LA * kABytes;
+    static constexpr int kBar = kA + LA * kSlotA;
     static constexpr int kNumBars = LB + LA + LA + LB + 1;  // full, ready, done (per ring), accfull
     static constexpr int kMisc = kBar + kNumBars * 8;
     static constexpr int kTotal = kMisc + 32;
     static constexpr int kAlloc = kTotal + 1024;  // slack for aligning the base to 1024
-    static constexpr int kTmemCols = BN < 32 ? 32 : BN;
+    static constexpr int kTmemCols = KM * (BN < 32 ? 32 : BN);
     static_assert(kAlloc <= 227 * 1024, "the rings fit a CTA's shared memory");
     static_assert(kBBytes % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-    static_assert(BN * kOutK * 4 <= LB * kBBytes, "the split partials fit the gradient ring");
+    static_assert(BN * kOutK * 4 <= LB * kBBytes, "the split partials or the output tiles fit the gradient ring");
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "TMEM allocations are powers of two");
 };
 
@@ -108,11 +115,13 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 
 // OG: G is a multiple of 64, so a thread's 64 k lie inside one scale group;
 // otherwise one scale per 16 k (G is a multiple of 16).
-template <int BN, int LB, int LA, int DQ, int MINB, bool OG>
+template <int BN, int LB, int LA, int DQ, int MINB, int KM, bool OG>
 __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
     w4a16_dgrad_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
                        const __grid_constant__ DgradParams p) {
-    using L = DgradLayout<BN, LB, LA>;
+    using L = DgradLayout<BN, LB, LA, KM>;
+    static_assert(DQ % KM == 0, "each group decodes one of the CTA's blocks of k");
+    constexpr int kTurn = DQ / KM;  // a group takes every kTurn-th stage
     constexpr int kScales = OG ? 1 : 4;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base_addr = smem_addr(smem_raw);
@@ -129,9 +138,8 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int kblk = blockIdx.y;
-    const int m0 = blockIdx.z * BN;
-    const int rows = min(BN, p.rows - m0);
+    const int m0 = blockIdx.z * p.tile_rows;
+    const int rows = min(p.tile_rows, p.rows - m0);
     const int split = blockIdx.x;
     const int ib = static_cast<int>((static_cast<int64_t>(split) * p.stages) / p.splits);
     const int ie = static_cast<int>((static_cast<int64_t>(split + 1) * p.stages) / p.splits);
@@ -140,7 +148,9 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
 
     // ---- decoding threads' state; the first loads go out before the setup below
     const int dw = warp - 2;
-    const int grp = dw >> 2;
+    const int kb = (dw >> 2) % KM;   // which of the CTA's blocks of k this group decodes
+    const int grp = (dw >> 2) / KM;  // its first stage
+    const int kblk = blockIdx.y * KM + (warp >= 2 ? kb : 0);
     const int t = static_cast<int>(threadIdx.x - 64) & 127;  // thread inside its group
     const int r = t & 63;                                    // column of the stage (contraction index)
     const int mb = t >> 6;                                   // which 64 of the CTA's 128 k
@@ -170,7 +180,7 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
 #pragma unroll
             for (int q = 0; q < kScales; ++q) sv[q] = __float2half(0.f);
         }
-        li += DQ;
+        li += kTurn;
     };
     uint4 c0[2], c1[2];
     __half s0[kScales], s1[kScales];
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
             mbar_init(&doneB[s], 1);
         }
         for (int s = 0; s < LA; ++s) {
-            mbar_init(&ready[s], kGroupWarps);
+            mbar_init(&ready[s], kGroupWarps * KM);
             mbar_init(&doneA[s], 1);
         }
         mbar_init(accfull, 1);
@@ -213,13 +223,13 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
             auto issue = [&](int l) {
                 const int i = ib + l, s = l % LB;
                 const int src = i >= p.NS ? 1 : 0;
-                mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(L::kBBytes));
+                mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.tile_rows * kDepth * 2));
                 tma_load_2d(smem + L::kB + s * L::kBBytes, src ? &tm1 : &tm0, (i - (src ? p.NS : 0)) * kDepth, m0,
                             &full[s]);
             };
-            // A pair of stages shares one (or, at the end of K, half a) run of two
-            // code tiles: fetched once, on the pair's first stage.
-            const uint32_t pair_bytes = static_cast<uint32_t>(min(2, p.KT - 2 * kblk)) * kTile;
+            // A pair of stages shares one run of 2 KM code tiles (fewer at the end of
+            // K): fetched once, on the pair's first stage.
+            const uint32_t pair_bytes = static_cast<uint32_t>(min(2 * KM, p.KT - 2 * kblk)) * kTile;
             auto prefetch = [&](int l) {
                 const int i = ib + l;
                 const int src = i >= p.NS ? 1 : 0;
@@ -254,14 +264,19 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
             for (int l = 0; l < nst; ++l) {
                 if (!wait_phase(&ready[sa], par, abort_flag, p.wait_limit, &g_dgrad_status)) break;
                 tc_fence_after_sync();
-                const uint64_t a = adesc0 + static_cast<uint64_t>(sa) * (kABytes >> 4);
+                const uint64_t a = adesc0 + static_cast<uint64_t>(sa) * (L::kSlotA >> 4);
                 const uint64_t b = bdesc0 + static_cast<uint64_t>(sb) * (L::kBBytes >> 4);
                 // 16 contraction rows per MMA: two 1024-byte atoms of the decoded
                 // tile, 32 bytes of every gradient row.
-                mma_f16_ss(tmem_acc, a, b, idesc, l > 0 ? 1u : 0u);
-                mma_f16_ss(tmem_acc, a + (2048 >> 4), b + 2, idesc, 1u);
-                mma_f16_ss(tmem_acc, a + 2 * (2048 >> 4), b + 4, idesc, 1u);
-                mma_f16_ss(tmem_acc, a + 3 * (2048 >> 4), b + 6, idesc, 1u);
+#pragma unroll
+                for (int h = 0; h < KM; ++h) {
+                    const uint64_t ah = a + h * (kABytes >> 4);
+                    const uint32_t acc = tmem_acc + h * BN;
+                    mma_f16_ss(acc, ah, b, idesc, l > 0 ? 1u : 0u);
+                    mma_f16_ss(acc, ah + (2048 >> 4), b + 2, idesc, 1u);
+                    mma_f16_ss(acc, ah + 2 * (2048 >> 4), b + 4, idesc, 1u);
+                    mma_f16_ss(acc, ah + 3 * (2048 >> 4), b + 6, idesc, 1u);
+                }
                 mma_commit(&doneA[sa]);
                 mma_commit(&doneB[sb]);
                 if (++sa == LA) {
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
     } else {
         // ------------------------------------------------------ decode + epilogue
         const uint32_t row_addr =
-            smem_addr(smem + L::kA) + static_cast<uint32_t>(mb * (kABytes / 2) + (r >> 3) * 1024 + (r & 7) * 128);
+            smem_addr(smem + L::kA) + static_cast<uint32_t>(kb * kABytes + mb * (kABytes / 2) + (r >> 3) * 1024 + (r & 7) * 128);
         auto stage = [&](int l, uint4 (&c)[2], __half (&sv)[kScales]) -> bool {
             const int sa = l % LA;
             const uint32_t raw[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
@@ -287,7 +302,7 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
             if (l >= LA && !warp_wait_phase(&doneA[sa], static_cast<uint32_t>((l / LA) - 1) & 1u, abort_flag,
                                             p.wait_limit, &g_dgrad_status))
                 return false;
-            const uint32_t dst = row_addr + static_cast<uint32_t>(sa * kABytes);
+            const uint32_t dst = row_addr + static_cast<uint32_t>(sa * L::kSlotA);
 #pragma unroll
             for (int q = 0; q < 8; ++q) sts128(dst + ((q ^ (r & 7)) << 4), v[q]);
             fence_proxy_async_smem();
@@ -301,9 +316,9 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
             return true;
         };
         // Two register slots, used alternately: codes stay in the registers they were loaded into.
-        for (int l = grp; l < nst; l += 2 * DQ) {
+        for (int l = grp; l < nst; l += 2 * kTurn) {
             if (!stage(l, c0, s0)) break;
-            if (l + DQ < nst && !stage(l + DQ, c1, s1)) break;
+            if (l + kTurn < nst && !stage(l + kTurn, c1, s1)) break;
         }
 
         // -------------------------------------------------- epilogue
@@ -318,10 +333,10 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
         if (lane == 0 && !have_acc) *tile_ok = 0;
         if (p.splits == 1) {
             if (have_acc) {
-                __half* stile = reinterpret_cast<__half*>(smem + L::kB);
-                for (int c = grp; c < n_mma / 16; c += DQ) {
+                __half* stile = reinterpret_cast<__half*>(smem + L::kB) + kb * BN * kOutK;  // [block of k][row][128]
+                for (int c = grp; c < n_mma / 16; c += kTurn) {
                     uint32_t v[16];
-                    tmem_ld_32x32b_x16(tmem_acc + tlane + c * 16, v);
+                    tmem_ld_32x32b_x16(tmem_acc + kb * BN + tlane + c * 16, v);
                     tmem_ld_wait();
 #pragma unroll
                     for (int x = 0; x < 16; ++x)
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
             }
         } else {
             float* red = reinterpret_cast<float*>(smem + L::kB);
-            for (int c = grp; c < BN / 16; c += DQ) {
+            for (int c = grp; c < BN / 16; c += kTurn) {  // (KM = 1)
                 uint32_t v[16];
                 if (have_acc && c * 16 < n_mma) {
                     tmem_ld_32x32b_x16(tmem_acc + tlane + c * 16, v);
@@ -352,18 +367,19 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
         tmem_dealloc(tmem_acc, L::kTmemCols);
     }
 
-    const int k0 = kblk * kOutK;
-    if (p.splits == 1) {
+    const int k0 = blockIdx.y * KM * kOutK;
+    if (KM > 1 || p.splits == 1) {
         if (*tile_ok) {
             const __half* stile = reinterpret_cast<const __half*>(smem + L::kB);
-            for (int o = threadIdx.x; o < rows * 16; o += static_cast<int>(blockDim.x)) {
-                const int rr = o >> 4;
-                const int cc = (o & 15) * 8;
+            for (int o = threadIdx.x; o < rows * 16 * KM; o += static_cast<int>(blockDim.x)) {
+                const int rr = o / (16 * KM);
+                const int cc = (o % (16 * KM)) * 8;
+                const __half* src = stile + (cc / kOutK) * BN * kOutK + rr * kOutK + cc % kOutK;
                 __half* dst = p.out + static_cast<int64_t>(m0 + rr) * p.K + k0 + cc;
                 if (p.vec_out && k0 + cc + 8 <= p.K) {
-                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(stile + rr * kOutK + cc);
+                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
                 } else {
-                    for (int e = 0; e < 8 && k0 + cc + e < p.K; ++e) dst[e] = stile[rr * kOutK + cc + e];
+                    for (int e = 0; e < 8 && k0 + cc + e < p.K; ++e) dst[e] = src[e];
                 }
             }
         }
@@ -433,18 +449,18 @@ __global__ void __launch_bounds__(kSlopeThreads)
 // ====================================================================== host
 
 struct DgradVariant {
-    int bn, threads, per_sm, smem;
+    int bn, km, per_sm, smem;
     const void* fn[2];  // G a multiple of 64, any G
     int (*launch[2])(const CUtensorMap&, const CUtensorMap&, const DgradParams&, dim3, int, cudaStream_t);
 };
 
-template <int BN, int LB, int LA, int DQ, int MINB, bool OG>
+template <int BN, int LB, int LA, int DQ, int MINB, int KM, bool OG>
 int launch_dgrad(const CUtensorMap& m0, const CUtensorMap& m1, const DgradParams& p, dim3 grid, int cluster_x,
                  cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(dgrad_threads(DQ), 1, 1);
-    cfg.dynamicSmemBytes = DgradLayout<BN, LB, LA>::kAlloc;
+    cfg.dynamicSmemBytes = DgradLayout<BN, LB, LA, KM>::kAlloc;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     int na = 0;
@@ -460,25 +476,27 @@ int launch_dgrad(const CUtensorMap& m0, const CUtensorMap& m1, const DgradParams
     }
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, w4a16_dgrad_kernel<BN, LB, LA, DQ, MINB, OG>, m0, m1, p) == cudaSuccess
+    return cudaLaunchKernelEx(&cfg, w4a16_dgrad_kernel<BN, LB, LA, DQ, MINB, KM, OG>, m0, m1, p) == cudaSuccess
                ? W4A16_OK
                : W4A16_ERR_CUDA;
 }
 
-template <int BN, int LB, int LA, int DQ, int MINB>
+template <int BN, int LB, int LA, int DQ, int MINB, int KM>
 DgradVariant make_dgrad() {
     return DgradVariant{BN,
-                        dgrad_threads(DQ),
+                        KM,
                         MINB,
-                        DgradLayout<BN, LB, LA>::kAlloc,
-                        {reinterpret_cast<const void*>(&w4a16_dgrad_kernel<BN, LB, LA, DQ, MINB, true>),
-                         reinterpret_cast<const void*>(&w4a16_dgrad_kernel<BN, LB, LA, DQ, MINB, false>)},
-                        {&launch_dgrad<BN, LB, LA, DQ, MINB, true>, &launch_dgrad<BN, LB, LA, DQ, MINB, false>}};
+                        DgradLayout<BN, LB, LA, KM>::kAlloc,
+                        {reinterpret_cast<const void*>(&w4a16_dgrad_kernel<BN, LB, LA, DQ, MINB, KM, true>),
+                         reinterpret_cast<const void*>(&w4a16_dgrad_kernel<BN, LB, LA, DQ, MINB, KM, false>)},
+                        {&launch_dgrad<BN, LB, LA, DQ, MINB, KM, true>,
+                         &launch_dgrad<BN, LB, LA, DQ, MINB, KM, false>}};
 }
 
-// <gradient rows, gradient stages, decoded stages, decoding groups, CTAs per SM>
-const DgradVariant kDgrad[] = {make_dgrad<32, 4, 4, 2, 2>(), make_dgrad<64, 4, 4, 2, 2>(),
-                               make_dgrad<128, 6, 4, 4, 1>(), make_dgrad<256, 5, 4, 4, 1>()};
+// <gradient rows, gradient stages, decoded stages, decoding groups, CTAs per SM, blocks of k per CTA>
+const DgradVariant kDgrad[] = {make_dgrad<32, 4, 4, 2, 2, 1>(), make_dgrad<64, 4, 4, 2, 2, 1>(),
+                               make_dgrad<128, 6, 4, 4, 1, 1>(), make_dgrad<256, 5, 4, 4, 1, 1>(),
+                               make_dgrad<256, 4, 3, 4, 1, 2>()};
 
 int prepare_dgrad_device() {
     static std::mutex mu;
@@ -510,9 +528,22 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
           w4a16_half* dA, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream) {
     int rc = prepare_dgrad_device();
     if (rc) return rc;
-    const int vi = M <= 32 ? 0 : (M <= 64 ? 1 : (M <= 128 ? 2 : 3));
+    const int64_t sms = sm_count() > 0 ? sm_count() : 148;
+    int vi = M <= 32 ? 0 : (M <= 64 ? 1 : (M <= 128 ? 2 : 3));
+    const int64_t MT = (M + kDgrad[vi].bn - 1) / kDgrad[vi].bn, NS = (N + kDepth - 1) / kDepth;
+    // Rows spread evenly over the tiles.
+    const int64_t tile_rows = ((M + MT - 1) / MT + 15) / 16 * 16;
+    if (vi == 3) {
+        // One or two blocks of k per CTA, by the rounds over the SMs times the cycles of a stage: shared-memory traffic
+        // at 128 bytes per clock (decoded tiles written and read, gradient tile written once and read per block).
+        auto cycles = [&](int64_t km) {
+            const int64_t ctas = ((K + kOutK * km - 1) / (kOutK * km)) * MT;
+            return ((ctas + sms - 1) / sms) * (256 * km + tile_rows * (1 + km));
+        };
+        if (cycles(2) < cycles(1)) vi = 4;
+    }
     const DgradVariant& v = kDgrad[vi];
-    const int64_t KB = (K + kOutK - 1) / kOutK, MT = (M + v.bn - 1) / v.bn, NS = (N + kDepth - 1) / kDepth;
+    const int64_t KB = (K + kOutK * v.km - 1) / (kOutK * v.km);
     if (KB > 65535 || MT > 65535) return W4A16_ERR_UNSUPPORTED;
     DgradParams p;
     std::memset(&p, 0, sizeof(p));
@@ -522,6 +553,7 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
     }
     p.out = reinterpret_cast<__half*>(dA);
     p.rows = static_cast<int32_t>(M);
+    p.tile_rows = static_cast<int32_t>(tile_rows);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.G = static_cast<int32_t>(G);
@@ -532,8 +564,8 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
     // Few tiles: split the contraction over a cluster while every rank keeps at
     // least eight stages and all CTAs are resident at once.
     int splits = 1;
-    const int64_t slots = static_cast<int64_t>(sm_count() > 0 ? sm_count() : 148) * v.per_sm;
-    while (splits < 8 && KB * MT * splits * 2 <= slots && p.stages >= splits * 16) splits *= 2;
+    const int64_t slots = sms * v.per_sm;
+    while (v.km == 1 && splits < 8 && KB * MT * splits * 2 <= slots && p.stages >= splits * 16) splits *= 2;
     p.splits = splits;
     p.prefetch = static_weights_enabled() ? 1 : 0;
     p.vec_out = aligned(dA, 16) ? 1 : 0;
@@ -541,7 +573,7 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
     p.stall_stage = injected_stall_stage();
     CUtensorMap maps[2];
     for (int i = 0; i < 2; ++i) {
-        rc = encode_activation_map(&maps[i], dC[i < sources ? i : 0], M, N, v.bn);
+        rc = encode_activation_map(&maps[i], dC[i < sources ? i : 0], M, N, static_cast<int>(tile_rows));
         if (rc) return rc;
     }
     const dim3 grid(static_cast<unsigned>(splits), static_cast<unsigned>(KB), static_cast<unsigned>(MT));
