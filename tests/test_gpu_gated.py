@@ -162,3 +162,26 @@ def test_helper_refuses_wrong_operands():
         w.gated_gemm(A.cpu(), c.wg, Sg, c.wu, Su, c.N, c.G)
     with pytest.raises(w.W4A16Error):
         w.gated_gemm(A, c.wg, Sg, c.wu, Su, c.N, c.G, act=9)
+
+
+@pytest.mark.parametrize("M,K,N,G,save", [(200, 264, 14336, 64, True), (300, 136, 8968, 48, False),
+                                          (513, 1112, 9480, 128, True), (2000, 200, 4104, 16, True)])
+def test_many_columns(M, K, N, G, save):
+    # the form with 128 output columns per CTA: odd rows, columns that end inside a block, one and several row tiles
+    check(Case(M, K, N, G, seed=M), act=M % 5, save=save)
+
+
+def test_a_stalled_stage_ends_with_the_timeout_status():
+    # the bounded waits of both tensor-core forms: the kernel latches the status and writes nothing
+    for M, N in ((40, 512), (300, 8192)):
+        c = Case(M, 1024, N, 64, seed=M)
+        out = torch.full((M, N), 7.0, dtype=torch.float16, device="cuda")
+        try:
+            w.w4a16_set_fault_injection(0, 2_000_000)  # (stages count from each CTA's start: all have a first one)
+            c.run(w.ACT_SILU, out=out)
+        finally:
+            w.w4a16_set_fault_injection(-1, 0)
+        assert w.device_status(clear=True) == w.ERR_TIMEOUT
+        assert (out == 7.0).all()
+        refs, bounds = f.gated(c.A, c.Wg, c.Wu, w.ACT_SILU)
+        assert f.worst(c.run(w.ACT_SILU).cpu().numpy(), refs[0], bounds[0]) <= 1

@@ -124,6 +124,13 @@ int decode_gated_launch(const void* A, const uint8_t* Wt_gate, const void* S_gat
 int decode_lora_launch(const LoraOperands& lora, const void* A, const uint8_t* Wt, const void* S, void* C, int64_t M,
                        int64_t N, int64_t K, int64_t G, cudaStream_t stream);
 
+// The gated projections of many rows, 128 output columns per CTA, and whether that
+// form is the faster one for the shape.
+bool wide_gated_takes(int64_t M, int64_t N);
+int wide_gated_launch(const w4a16_half* A, const uint8_t* Wt_gate, const w4a16_half* S_gate, const uint8_t* Wt_up,
+                      const w4a16_half* S_up, w4a16_half* H, w4a16_half* Pg, w4a16_half* Pu, int64_t M, int64_t N,
+                      int64_t K, int64_t G, int act, cudaStream_t stream);
+
 // Whether they take the shape (a scale group's index must fit their multiply-shift,
 // the weights' offsets 32 bits); the tensor-core kernel takes any.
 bool decode_takes(int64_t M, int64_t N, int64_t K, int64_t G);
