@@ -16,14 +16,15 @@
 //     barrier on the weight path), decodes them to fp16(q * s) and feeds them to
 //     m16n8k16 MMAs with the tokens as the 8-column operand;
 //   - the activations are staged once (or in pieces, when K is long) with only M
-//     rows: the operand columns past M read row M - 1, and their results are
-//     dropped;
+//     rows, one bulk copy per row (16 copies of 8 KB arrive in about 2 us; 16-byte
+//     copies by the threads took 7): the operand columns past M read row M - 1, and
+//     their results are dropped;
 //   - the KS partial tiles are added in order through shared memory.
 // A chunk of 32 k is four words of 8 codes; inside an MMA the order of k is free as
-// long as both operands use it, so thread t of a quad takes k = 32t + 8w .. + 7 of
-// a block for word w, and the staged block holds the 16-byte unit of (t, w) at
-// 64w + 16t: with rows 64 bytes (mod 128) apart, the eight lanes of one
-// shared-memory phase read eight distinct 16-byte banks.
+// long as both operands use it, so thread t of a quad takes k = 32t + 8v .. + 7 of
+// a block for step w, with v = w for t = 0, 1 and v = w ^ 1 for t = 2, 3: with rows
+// 32 bytes (mod 128) apart, the eight lanes of one shared-memory phase then read
+// eight distinct 16-byte banks.
 //
 // Adapters (FORM kLora): after its blocks of K a warp goes on with the adapter
 // ranks as more k: for each token m (every KS-th) the rows of LB[ids[m]] of its 16
@@ -43,6 +44,7 @@
 #include "epilogue.cuh"
 #include "ptx.cuh"
 #include "w4a16_internal.h"
+#include "waits.cuh"
 
 namespace w4a16 {
 
@@ -71,8 +73,11 @@ struct DecodeParams {
     int32_t row_bytes;        // staged activation row
     uint32_t g_magic;         // floor(k / G) == (k * g_magic) >> 32
     int32_t act, prefetch;
+    long long wait_limit;
     LoraOperands lora;
 };
+
+__device__ int g_decode_status;  // latched device-side error (0 = none)
 
 // 16 bytes of codes, read once: past L1.
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
@@ -103,7 +108,9 @@ __device__ __forceinline__ uint32_t keep_finite(uint32_t x) { return x & ~((nonf
 template <int MT, int FORM, bool FINE>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const __grid_constant__ DecodeParams p) {
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ int fix;  // adapters: an infinity or NaN was left out
+    __shared__ int fix;     // adapters: an infinity or NaN was left out
+    __shared__ int failed;  // the wait for the activations ran out
+    __shared__ __align__(8) uint64_t landed;
     constexpr bool LORA = FORM == kLora;
     constexpr int kNS = FINE ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -159,7 +166,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
     };
 
     Block blk[kAhead];
-    if (threadIdx.x == 0) fix = 0;
+    if (threadIdx.x == 0) {
+        fix = 0;
+        failed = 0;
+        mbar_init(&landed, 1);
+        fence_mbar_init();
+    }
     // (Adapters: this launch follows the kernel that makes V, which lets it start only
     // once everything before it is complete; weights, scales and activations are read
     // at once, not through L1, and it waits for that kernel just before it reads V.)
@@ -179,30 +191,37 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
     for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[u][j][0] = acc[u][j][1] = acc[u][j][2] = acc[u][j][3] = 0.f;
-    uint32_t arow[MT];
+    // Where this thread's units of a row start, for even and odd steps.
+    uint32_t aeven[MT], aodd[MT];
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-        arow[j] = smem_addr(sm) + static_cast<uint32_t>(min(8 * j + g, p.M - 1) * p.row_bytes + 16 * t);
+    for (int j = 0; j < MT; ++j) {
+        const uint32_t base = smem_addr(sm) + static_cast<uint32_t>(min(8 * j + g, p.M - 1) * p.row_bytes + 64 * t);
+        aeven[j] = base + 16 * (t >> 1);
+        aodd[j] = base - 16 * (t >> 1);
+    }
 
     for (int i0 = 0; i0 < p.iters; i0 += p.piece) {
         // Stage the activations of blocks [i0 * KS, (i0 + piece) * KS): zero past K.
         {
-            const int b0 = i0 * p.KS;
-            const int units = (min(p.KB, b0 + p.piece * p.KS) - b0) * 16;  // 16-byte units per row
-            if (i0 > 0) __syncthreads();  // the piece before is consumed
-            // (Asynchronous copies: all of a thread's 16-byte units are in flight at once.)
-            for (int m = 0; m < p.M; ++m) {
-                const __half* src = p.A + static_cast<int64_t>(m) * p.K + b0 * kBlockK;
-                uint8_t* dst = sm + m * p.row_bytes;
-                for (int c = threadIdx.x; c < units; c += static_cast<int>(blockDim.x)) {
-                    const bool in = b0 * kBlockK + 8 * c < p.K;
-                    cp_async16(dst + (c >> 4) * 256 + ((c & 3) * 4 + ((c >> 2) & 3)) * 16, in ? src + 8 * c : p.A,
-                               in ? 16u : 0u);
-                }
+            const int k0 = i0 * p.KS * kBlockK;
+            const int blocks = min(p.KB - i0 * p.KS, p.piece * p.KS);
+            const int have = min(p.K - k0, blocks * kBlockK);  // (a multiple of 8)
+            __syncthreads();  // the barrier is set up, or the piece before is consumed
+            if (threadIdx.x == 0) {
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(&landed, static_cast<uint32_t>(p.M * have * 2));
+                for (int m = 0; m < p.M; ++m)
+                    bulk_g2s(sm + m * p.row_bytes, p.A + static_cast<int64_t>(m) * p.K + k0,
+                             static_cast<uint32_t>(have * 2), &landed);
             }
-            cp_async_commit();
-            cp_async_wait<0>();
-            __syncthreads();
+            const int tail = (blocks * kBlockK - have) / 8;  // 16-byte units past K
+            for (int c = threadIdx.x; c < p.M * tail; c += static_cast<int>(blockDim.x))
+                *reinterpret_cast<uint4*>(sm + (c / tail) * p.row_bytes + have * 2 + (c % tail) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t par = static_cast<uint32_t>(i0 / p.piece) & 1u;
+            if (!warp_wait_phase(&landed, par, &failed, p.wait_limit, &g_decode_status))
+                warp_drain_phase(&landed, par, &g_decode_status);  // (no copy may outlive the CTA)
+            if (tail > 0) __syncthreads();  // (the zeros)
         }
         const int iend = min(p.iters, i0 + p.piece);
         uint32_t off = static_cast<uint32_t>(kh) * 256;  // this warp's block in the staged piece
@@ -212,8 +231,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
             for (int d = 0; d < kAhead; ++d) {
                 Block& x = blk[d];
                 if (left > 0) {  // (the same for the whole warp)
-                    const uint32_t aw[4] = {x.a.x, x.a.y, x.a.z, x.a.w};
-                    const uint32_t bw[4] = {x.b.x, x.b.y, x.b.z, x.b.w};
+                    // (steps in this thread's order)
+                    const bool odd = t & 2;
+                    const uint32_t aw[4] = {odd ? x.a.y : x.a.x, odd ? x.a.x : x.a.y, odd ? x.a.w : x.a.z,
+                                            odd ? x.a.z : x.a.w};
+                    const uint32_t bw[4] = {odd ? x.b.y : x.b.x, odd ? x.b.x : x.b.y, odd ? x.b.w : x.b.z,
+                                            odd ? x.b.z : x.b.w};
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const uint4 qa = dequant_word(aw[w], __half2half2(__ushort_as_half(x.sa[FINE ? w >> 1 : 0])));
@@ -222,7 +245,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
                         const uint32_t f1[4] = {qa.z, qb.z, qa.w, qb.w};
 #pragma unroll
                         for (int j = 0; j < MT; ++j) {
-                            const uint4 y = lds128(arow[j] + off + 64 * w);
+                            const uint4 y = lds128((w & 1 ? aodd[j] : aeven[j]) + off + 16 * w);
                             mma_m16n8k16(acc[0][j], f0, y.x, y.y);
                             mma_m16n8k16(acc[1][j], f1, y.z, y.w);
                         }
@@ -285,7 +308,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
                 make_float4(acc[0][j][0], acc[0][j][1], acc[0][j][2], acc[0][j][3]);
     }
     __syncthreads();
-    if (kh > 0 || !active) return;
+    if (kh > 0 || !active || *const_cast<volatile int*>(&failed)) return;
     for (int s = 1; s < p.KS; ++s) {  // in order: deterministic
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
@@ -395,13 +418,14 @@ int decode_launch(DecodeParams& p, DecodeForm form, int64_t M, int64_t N, int64_
     int red = 0, blocks = 0;  // bytes of the partial tiles; 128-deep blocks of activations that fit
     for (;; --p.KS) {
         red = (p.KS - 1) * p.P * mt * 512;
-        blocks = ((kMaxSmem - red) / p.M - 64) / 256;
+        blocks = ((kMaxSmem - red) / p.M - 32) / 256;
         if (blocks >= p.KB || blocks >= p.KS * kAhead || p.KS == 1) break;
     }
     p.iters = (p.KB + p.KS - 1) / p.KS;
     p.piece = blocks >= p.KB ? (p.iters + kAhead - 1) / kAhead * kAhead : blocks / p.KS / kAhead * kAhead;
-    p.row_bytes = std::min(p.piece * p.KS, p.KB) * 256 + 64;
+    p.row_bytes = std::min(p.piece * p.KS, p.KB) * 256 + 32;
     if (!group_magic(G, static_cast<int64_t>(p.KB) * kBlockK, &p.g_magic)) return W4A16_ERR_UNSUPPORTED;
+    p.wait_limit = device_wait_limit();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tiles + P - 1) / P), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(p.P * p.KS * 32), 1, 1);
@@ -421,6 +445,16 @@ bool decode_takes(int64_t M, int64_t N, int64_t K, int64_t G) {
     uint32_t magic;
     return M <= kSkinnyMaxM && w4a16_tiled_bytes(K, N) < (int64_t(1) << 32) &&
            group_magic(G, (K + 127) / 128 * 128, &magic);
+}
+
+int decode_device_status(bool clear) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_decode_status, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && v != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_decode_status, &zero, sizeof(int)) != cudaSuccess) return -1;
+    }
+    return v;
 }
 
 int decode_gated_launch(const void* A, const uint8_t* Wt_gate, const void* S_gate, const uint8_t* Wt_up,

@@ -1643,8 +1643,9 @@ extern "C" int w4a16_device_status(int clear) {
     const int vm = moe_device_status(clear != 0);
     const int vd = dgrad_device_status(clear != 0);
     const int vl = lora_device_status(clear != 0);
-    if (vs < 0 || vq < 0 || vm < 0 || vd < 0 || vl < 0) return W4A16_ERR_CUDA;
-    for (int x : {v, vs, vq, vm, vd})
+    const int vx = decode_device_status(clear != 0);
+    if (vs < 0 || vq < 0 || vm < 0 || vd < 0 || vl < 0 || vx < 0) return W4A16_ERR_CUDA;
+    for (int x : {v, vs, vq, vm, vd, vx})
         if (x != 0) return x;
     return vl;
 }

@@ -131,6 +131,8 @@ int wide_gated_launch(const w4a16_half* A, const uint8_t* Wt_gate, const w4a16_h
                       const w4a16_half* S_up, w4a16_half* H, w4a16_half* Pg, w4a16_half* Pu, int64_t M, int64_t N,
                       int64_t K, int64_t G, int act, cudaStream_t stream);
 
+int decode_device_status(bool clear);
+
 // Whether they take the shape (a scale group's index must fit their multiply-shift,
 // the weights' offsets 32 bits); the tensor-core kernel takes any.
 bool decode_takes(int64_t M, int64_t N, int64_t K, int64_t G);
