@@ -20,7 +20,7 @@
 // 32-deep blocks, read both operands straight from global memory into MMA
 // fragments (16 bytes per lane: inside a block the order of k is free as long
 // as both operands use it), and add their fp32 partials in warp order through
-// shared memory. Rows of another adapter ride along and are not written. It is
+// shared memory. It is
 // bound by latency at decode sizes and by reading A and the adapters (L2) at
 // prompt sizes. Extra CTAs behind the row groups list the distinct adapters of
 // each token tile of the tensor-core product.
@@ -153,11 +153,15 @@ __global__ void __launch_bounds__(W * 32) lora_down_kernel(const DownParams p) {
         float acc[RT][4];
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-        // Rows past M and ranks past R read a row that exists; their sums are not
-        // written. (No load is conditional: a branch around a load would wait for
-        // its value where the two paths meet.)
-        const __half* a0 = p.A + static_cast<int64_t>(min(m0 + g, p.M - 1)) * p.K + 8 * t;
-        const __half* a1 = p.A + static_cast<int64_t>(min(m0 + g + 8, p.M - 1)) * p.K + 8 * t;
+        // Rows of another adapter (or past M) read this adapter's first row along with
+        // it, ranks past R the last rank; their sums are not written. (No load is
+        // conditional: a branch around a load would wait for its value where the two
+        // paths meet.)
+        const int lead = __ffs(leaders) - 1;
+        const int row0 = __shfl_sync(0xffffffffu, mine, g) == id ? g : lead;
+        const int row1 = __shfl_sync(0xffffffffu, mine, g + 8) == id ? g + 8 : lead;
+        const __half* a0 = p.A + static_cast<int64_t>(m0 + row0) * p.K + 8 * t;
+        const __half* a1 = p.A + static_cast<int64_t>(m0 + row1) * p.K + 8 * t;
         const __half* lb[RT];
 #pragma unroll
         for (int j = 0; j < RT; ++j)
