@@ -688,18 +688,29 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
 
 }  // namespace
 
-bool wide_gated_takes(int64_t M, int64_t N) {
+// Whether the gated projections run here rather than on the form with 64 output
+// columns per CTA (half the work per CTA and stage, twice the CTAs, and a K split for
+// one row tile). Cycles of a launch on either side, fitted to measured launches: a
+// CTA's start and epilogue, then its stages (decoding bounds a stage here from below
+// at 820), and the exchange of a K split. Measured, this form against the other:
+// 2048 x 4096 -> 14336 417 / 461 us; 700 x 800 -> 9000 26.9 / 39.6; 333 x 1112 -> 2856
+// (G = 48) 15.7 / 18.2; 96 x 4096 -> 14336 38.3 / 41.1; 150 x 4096 -> 4096 36.4 / 20.0;
+// 500 x 2048 -> 4096 21.7 / 19.4.
+bool wide_gated_takes(int64_t M, int64_t N, int64_t K, int64_t G, int64_t row_tile, int64_t splits,
+                      int64_t ctas_per_sm) {
     const int64_t sms = sm_count() > 0 ? sm_count() : 148;
-    const int64_t blocks = (N + kOutK - 1) / kOutK;
-    if (M <= 128 || blocks > 65535) return false;
+    const int64_t blocks = (N + kOutK - 1) / kOutK, KT = (K + kDepth - 1) / kDepth;
+    if (M <= 64 || blocks > 65535) return false;
     int64_t mt = 0;
-    const int64_t wide = wide_cost(M, blocks, 2, sms, &mt);
-    // The form with 64 output columns per CTA: half the work per CTA and stage, twice
-    // the CTAs. Its stage costs about 800 on this scale (2048 x 4096 -> 14336: 13
-    // rounds in 461 us against 7 in 417).
-    const int64_t mt1 = (M + 255) / 256;
-    const int64_t narrow = ((((N + 63) / 64) * mt1 + sms - 1) / sms) * 800 * std::min<int64_t>(M, 256) / 256;
-    return wide < narrow;
+    wide_cost(M, blocks, 2, sms, &mt);
+    const int64_t wide = ((blocks * mt + sms - 1) / sms) *
+                         (15000 + KT * std::max<int64_t>(820, 4 * rows_of_tile(M, mt) + 200));
+    const int64_t ctas = ((N + 63) / 64) * ((M + row_tile - 1) / row_tile) * splits;
+    int64_t stage = row_tile <= 128 ? 1170 : 750;  // (small row tiles: two CTAs per SM)
+    if (G % kDepth) stage += stage / 4;            // eight scales per stage and thread
+    const int64_t other = ((ctas + sms * ctas_per_sm - 1) / (sms * ctas_per_sm)) * (16000 + (KT / splits) * stage) +
+                          (splits > 1 ? 12000 : 0);
+    return wide < other;
 }
 
 int wide_gated_launch(const w4a16_half* A, const uint8_t* Wt_gate, const w4a16_half* S_gate, const uint8_t* Wt_up,

@@ -1552,11 +1552,11 @@ int gated_gemm(const w4a16_half* A_dev, const uint8_t* Wt_gate, const w4a16_half
                int64_t K, int64_t G, int act, cudaStream_t stream) {
     if (decode_takes(M, N, K, G))
         return decode_gated_launch(A_dev, Wt_gate, S_gate, Wt_up, S_up, H_dev, Pg_dev, Pu_dev, M, N, K, G, act, stream);
-    if (wide_gated_takes(M, N))
-        return wide_gated_launch(A_dev, Wt_gate, S_gate, Wt_up, S_up, H_dev, Pg_dev, Pu_dev, M, N, K, G, act, stream);
     Plan plan;
     int rc = plan_dense(M, N, K, &plan, true, 0, 0, kGatedInt4);
     if (rc) return rc;
+    if (wide_gated_takes(M, N, K, G, plan.bn, plan.splits, plan.ctas_per_sm))
+        return wide_gated_launch(A_dev, Wt_gate, S_gate, Wt_up, S_up, H_dev, Pg_dev, Pu_dev, M, N, K, G, act, stream);
     Params p;
     std::memset(&p, 0, sizeof(p));
     p.wt[0] = Wt_gate;

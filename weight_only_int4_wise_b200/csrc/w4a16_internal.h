@@ -125,8 +125,9 @@ int decode_lora_launch(const LoraOperands& lora, const void* A, const uint8_t* W
                        int64_t N, int64_t K, int64_t G, cudaStream_t stream);
 
 // The gated projections of many rows, 128 output columns per CTA, and whether that
-// form is the faster one for the shape.
-bool wide_gated_takes(int64_t M, int64_t N);
+// form is the faster one for the shape, given the other form's launch.
+bool wide_gated_takes(int64_t M, int64_t N, int64_t K, int64_t G, int64_t row_tile, int64_t splits,
+                      int64_t ctas_per_sm);
 int wide_gated_launch(const w4a16_half* A, const uint8_t* Wt_gate, const w4a16_half* S_gate, const uint8_t* Wt_up,
                       const w4a16_half* S_up, w4a16_half* H, w4a16_half* Pg, w4a16_half* Pu, int64_t M, int64_t N,
                       int64_t K, int64_t G, int act, cudaStream_t stream);
