@@ -201,3 +201,15 @@ def test_a_stalled_stage_ends_with_the_timeout_status():
         again = w.gemm_dgrad(dC, layer.wt, layer.S, 256, 64, out=out)
         ref, err = f.product(dC.cpu().numpy(), layer.W.T)
         assert f.worst(again.cpu().numpy(), ref, f.half_step(ref) + 1.001 * err) <= 1
+
+
+@pytest.mark.parametrize("M,K,N,G", [(300, 19288, 72, 48), (2000, 2680, 136, 64), (1030, 5000, 264, 128), (260, 19400, 8, 16)])
+def test_two_blocks_per_cta(M, K, N, G):
+    # enough output blocks that a CTA takes two; the last one alone, ending inside the block
+    layer = Layer(K, N, G, seed=K)
+    dC = gradient(M, N, M)
+    flat, dA, pad = guarded_output(M, K)
+    w.gemm_dgrad(dev(dC), layer.wt, layer.S, K, G, out=dA)
+    ref, err = f.product(dC, layer.W.T)
+    assert f.worst(dA.cpu().numpy(), ref, f.half_step(ref) + 1.001 * err) <= 1
+    assert guards_intact(flat, pad, M * K)

@@ -185,3 +185,15 @@ def test_a_stalled_stage_ends_with_the_timeout_status():
         assert (out == 7.0).all()
         refs, bounds = f.gated(c.A, c.Wg, c.Wu, w.ACT_SILU)
         assert f.worst(c.run(w.ACT_SILU).cpu().numpy(), refs[0], bounds[0]) <= 1
+
+
+@pytest.mark.parametrize("M,K,N,G", [(16, 14336, 64, 128), (9, 14344, 72, 48), (13, 8200, 136, 80), (1, 30008, 64, 64),
+                                     (16, 20000, 8, 32)])
+def test_long_contraction_at_decode_sizes(M, K, N, G):
+    # K too long for the activations to be staged at once: several pieces, the last one partial
+    check(Case(M, K, N, G, seed=M), act=M % 5, save=True)
+
+
+@pytest.mark.parametrize("M,K,N,G", [(1, 64, 40000, 64), (16, 136, 36008, 16), (7, 8, 4104, 16), (200, 8, 14336, 16)])
+def test_many_columns_short_contraction(M, K, N, G):
+    check(Case(M, K, N, G, seed=M), act=w.ACT_SILU, save=False)

@@ -247,3 +247,10 @@ def test_no_rows_and_wrong_operands():
         w.lora_gemm(A, wt, S, N, G, LA, LB, ids, sc, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(w.W4A16Error):
         w.lora_gemm(A, wt, S, N, G, LA[:, :4].contiguous(), LB[:, :, :4].contiguous(), ids, sc)  # rank 4
+
+
+@pytest.mark.parametrize("M,K,N,G,L,R", [(16, 14336, 64, 128, 5, 16), (11, 14344, 72, 48, 3, 24), (16, 136, 70008, 16, 4, 8),
+                                         (1, 64, 80000, 64, 2, 8), (9, 8, 4104, 16, 2, 128), (40, 14336, 72, 64, 3, 8),
+                                         (1100, 264, 136, 64, 3, 40), (1030, 4096, 264, 128, 70, 16)])
+def test_long_and_wide(M, K, N, G, L, R):
+    Case(M, K, N, G, L, R, seed=M + K).check()
