@@ -558,12 +558,22 @@ def gemm_w8(A, wt8, S, N: int, G: int, out=None, stream=None):
     return C
 
 
-# The helpers below run in front of launches of a few microseconds: the checks are plain comparisons, and messages
-# are put together only for an error.
+# The helpers below run in front of launches of a few microseconds: the checks are plain comparisons, messages are
+# put together only for an error, and nothing is imported or wrapped unless the call needs it.
 
-def _torch_half():
+_torch = None        # the torch module, once a helper has been called
+_raw_stream = None   # device index -> raw handle of torch's current stream
+_this_device = None  # () -> index of torch's current device
+
+
+def _setup():
+    global _torch, _raw_stream, _this_device
     import torch
-    return torch.float16
+    load()
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _current_stream
+    _this_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
+    return torch
 
 
 def _refuse(name, t, dtype, shape, device):
@@ -576,30 +586,19 @@ def _refuse(name, t, dtype, shape, device):
 
 def _operand(name, t, dtype, shape, device):
     """A dense operand of a given type and shape on a device (a dense copy if it is strided)."""
-    if t.get_device() != device or t.dtype is not dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         _refuse(name, t, dtype, shape, device)
     return t if t.is_contiguous() else t.contiguous()
-
-
-def _rows_operand(name, t, dtype):
-    """The CUDA matrix that a call's rows come from: (device index, rows, columns)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {list(t.shape)}")
-    return t.get_device(), t.shape[0], t.shape[1]
 
 
 def _scales(name, wt, S, K, N, G, half, device):
     """Checks tiled int4 weights [K, N] against their sizes; returns the dense scales."""
     if G <= 0:
         raise W4A16Error(ERR_INVALID_ARG, name)
-    if (wt.get_device() != device or wt.element_size() != 1 or not wt.is_contiguous()
-            or wt.numel() != ((K + 63) // 64) * ((N + 127) // 128) * 4096):
+    if (wt.numel() != ((K + 63) // 64) * ((N + 127) // 128) * 4096 or wt.element_size() != 1
+            or not wt.is_contiguous() or wt.get_device() != device):
         raise ValueError(f"{name} must be the tiled layout of [{K}, {N}] codes (dense uint8) on CUDA device {device}")
-    if S.get_device() != device or S.dtype is not half or S.shape != ((K + G - 1) // G, N):
+    if S.dtype is not half or S.shape != ((K + G - 1) // G, N) or S.get_device() != device:
         _refuse(f"the scales of {name}", S, half, ((K + G - 1) // G, N), device)
     return S if S.is_contiguous() else S.contiguous()
 
@@ -607,41 +606,34 @@ def _scales(name, wt, S, K, N, G, half, device):
 def _output(name, out, shape, like):
     if out is None:
         return like.new_empty(shape)
-    if (out.get_device() != like.get_device() or out.dtype is not like.dtype or out.shape != shape
-            or not out.is_contiguous()):
+    if (out.dtype is not like.dtype or out.shape != shape or not out.is_contiguous()
+            or out.get_device() != like.get_device()):
         raise ValueError(f"{name} must be a dense {like.dtype} tensor of shape {list(shape)} on {like.device}")
     return out
 
 
-class _launch_on:
-    """A device and, if one is given, a stream (a torch stream or a raw handle) made current for one call, so that
-    the copies and buffers that the call makes belong to the stream its kernels run on. Yields the stream's raw
-    handle."""
-
-    __slots__ = ("device", "stream", "guards")
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, ()
-
-    def __enter__(self):
-        import torch
-        if self.stream is None and self.device == torch.cuda.current_device():
-            return _current_stream(self.device)
-        self.guards = [torch.cuda.device(self.device)]
-        self.guards[0].__enter__()
-        if self.stream is None:
-            return _current_stream(self.device)
-        raw = _stream(self.stream)
-        st = self.stream if isinstance(self.stream, torch.cuda.Stream) else (
-            torch.cuda.ExternalStream(raw, device=self.device) if raw else torch.cuda.default_stream(self.device))
-        self.guards.append(torch.cuda.stream(st))
-        self.guards[1].__enter__()
-        return raw
-
-    def __exit__(self, *exc):
-        for guard in reversed(self.guards):
-            guard.__exit__(*exc)
-        return False
+def _launch(call, name, rows, stream, *args):
+    """call(rows, device, raw stream, *args) with the rows' device and, if one is given, `stream` (a torch stream or
+    a raw handle) current, so that the copies and buffers that the call makes belong to the stream its kernels run
+    on."""
+    torch = _torch or _setup()
+    if not rows.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if rows.dtype is not torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {rows.dtype}")
+    if rows.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {list(rows.shape)}")
+    device = rows.get_device()
+    if stream is None and device == _this_device():
+        return call(rows if rows.is_contiguous() else rows.contiguous(), device, _raw_stream(device), *args)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(rows.contiguous(), device, _raw_stream(device), *args)
+        raw = _stream(stream)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            return call(rows.contiguous(), device, raw, *args)
 
 
 def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_SILU, save: bool = False, out=None,
@@ -649,39 +641,43 @@ def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_S
     """H [M, N] fp16 = act(A x W_gate) * (A x W_up) from activations A [M, K] fp16 and two tiled weight
     matrices [K, N] with scales [ceil(K/G), N]; one rounding. With save=True returns (H, gate, up), the two
     projections in fp16 as gated_gemm_backward reads them."""
-    half = _torch_half()
-    device, M, K = _rows_operand("A", A, half)
-    with _launch_on(device, stream) as st:
-        A = A if A.is_contiguous() else A.contiguous()
-        S_gate = _scales("wt_gate", wt_gate, S_gate, K, N, G, half, device)
-        S_up = _scales("wt_up", wt_up, S_up, K, N, G, half, device)
-        H = _output("out", out, (M, N), A)
-        Pg = _output("out_gate", out_gate, (M, N), A) if save else None
-        Pu = _output("out_up", out_up, (M, N), A) if save else None
-        if M:  # (an empty tensor has no address to pass)
-            rc = (_lib or load()).w4a16_gated_gemm(A.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(),
-                                                   wt_up.data_ptr(), S_up.data_ptr(), H.data_ptr(),
-                                                   Pg.data_ptr() if save else None, Pu.data_ptr() if save else None,
-                                                   M, N, K, G, act, flags, st)
-            if rc != OK:
-                raise W4A16Error(rc, "w4a16_gated_gemm")
+    return _launch(_gated_gemm, "A", A, stream, wt_gate, S_gate, wt_up, S_up, N, G, act, save, out, out_gate, out_up,
+                   flags)
+
+
+def _gated_gemm(A, device, st, wt_gate, S_gate, wt_up, S_up, N, G, act, save, out, out_gate, out_up, flags):
+    M, K = A.shape
+    half = A.dtype
+    S_gate = _scales("wt_gate", wt_gate, S_gate, K, N, G, half, device)
+    S_up = _scales("wt_up", wt_up, S_up, K, N, G, half, device)
+    shape = (M, N)
+    H = _output("out", out, shape, A)
+    Pg = Pu = pg = pu = None
+    if save:
+        Pg, Pu = _output("out_gate", out_gate, shape, A), _output("out_up", out_up, shape, A)
+        pg, pu = Pg.data_ptr(), Pu.data_ptr()
+    if M:  # (an empty tensor has no address to pass)
+        rc = _lib.w4a16_gated_gemm(A.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(), wt_up.data_ptr(),
+                                   S_up.data_ptr(), H.data_ptr(), pg, pu, M, N, K, G, act, flags, st)
+        if rc != OK:
+            raise W4A16Error(rc, "w4a16_gated_gemm")
     return (H, Pg, Pu) if save else H
 
 
 def gemm_dgrad(dC, wt, S, K: int, G: int, out=None, flags: int = 0, stream=None):
     """dA [M, K] fp16 = dC [M, N] x W^T, the gradient of gemm's input, from the forward product's tiled weights
     and scales [ceil(K/G), N]."""
-    half = _torch_half()
-    device, M, N = _rows_operand("dC", dC, half)
-    with _launch_on(device, stream) as st:
-        dC = dC if dC.is_contiguous() else dC.contiguous()
-        S = _scales("wt", wt, S, K, N, G, half, device)
-        dA = _output("out", out, (M, K), dC)
-        if M:
-            rc = (_lib or load()).w4a16_gemm_dgrad(dC.data_ptr(), wt.data_ptr(), S.data_ptr(), dA.data_ptr(), M, N,
-                                                   K, G, flags, st)
-            if rc != OK:
-                raise W4A16Error(rc, "w4a16_gemm_dgrad")
+    return _launch(_gemm_dgrad, "dC", dC, stream, wt, S, K, G, out, flags)
+
+
+def _gemm_dgrad(dC, device, st, wt, S, K, G, out, flags):
+    M, N = dC.shape
+    S = _scales("wt", wt, S, K, N, G, dC.dtype, device)
+    dA = _output("out", out, (M, K), dC)
+    if M:
+        rc = _lib.w4a16_gemm_dgrad(dC.data_ptr(), wt.data_ptr(), S.data_ptr(), dA.data_ptr(), M, N, K, G, flags, st)
+        if rc != OK:
+            raise W4A16Error(rc, "w4a16_gemm_dgrad")
     return dA
 
 
@@ -689,23 +685,26 @@ def gated_gemm_backward(dH, gate, up, wt_gate, S_gate, wt_up, S_up, K: int, G: i
                         out_gate=None, out_up=None, flags: int = 0, stream=None):
     """Backward of gated_gemm with frozen weights: (dA [M, K], d_gate [M, N], d_up [M, N]) from the gradient dH
     [M, N] and the projections that gated_gemm(..., save=True) returned."""
-    half = _torch_half()
-    device, M, N = _rows_operand("dH", dH, half)
-    with _launch_on(device, stream) as st:
-        dH = dH if dH.is_contiguous() else dH.contiguous()
-        gate = _operand("gate", gate, half, (M, N), device)
-        up = _operand("up", up, half, (M, N), device)
-        S_gate = _scales("wt_gate", wt_gate, S_gate, K, N, G, half, device)
-        S_up = _scales("wt_up", wt_up, S_up, K, N, G, half, device)
-        dA = _output("out", out, (M, K), dH)
-        dG, dU = _output("out_gate", out_gate, (M, N), dH), _output("out_up", out_up, (M, N), dH)
-        if M:
-            rc = (_lib or load()).w4a16_gated_gemm_backward(
-                dH.data_ptr(), gate.data_ptr(), up.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(),
-                wt_up.data_ptr(), S_up.data_ptr(), dG.data_ptr(), dU.data_ptr(), dA.data_ptr(), M, N, K, G, act,
-                flags, st)
-            if rc != OK:
-                raise W4A16Error(rc, "w4a16_gated_gemm_backward")
+    return _launch(_gated_gemm_backward, "dH", dH, stream, gate, up, wt_gate, S_gate, wt_up, S_up, K, G, act, out,
+                   out_gate, out_up, flags)
+
+
+def _gated_gemm_backward(dH, device, st, gate, up, wt_gate, S_gate, wt_up, S_up, K, G, act, out, out_gate, out_up,
+                         flags):
+    M, N = shape = tuple(dH.shape)
+    half = dH.dtype
+    gate = _operand("gate", gate, half, shape, device)
+    up = _operand("up", up, half, shape, device)
+    S_gate = _scales("wt_gate", wt_gate, S_gate, K, N, G, half, device)
+    S_up = _scales("wt_up", wt_up, S_up, K, N, G, half, device)
+    dA = _output("out", out, (M, K), dH)
+    dG, dU = _output("out_gate", out_gate, shape, dH), _output("out_up", out_up, shape, dH)
+    if M:
+        rc = _lib.w4a16_gated_gemm_backward(
+            dH.data_ptr(), gate.data_ptr(), up.data_ptr(), wt_gate.data_ptr(), S_gate.data_ptr(), wt_up.data_ptr(),
+            S_up.data_ptr(), dG.data_ptr(), dU.data_ptr(), dA.data_ptr(), M, N, K, G, act, flags, st)
+        if rc != OK:
+            raise W4A16Error(rc, "w4a16_gated_gemm_backward")
     return dA, dG, dU
 
 
@@ -714,34 +713,37 @@ def lora_gemm(A, wt, S, N: int, G: int, lora_A, lora_B, ids, scaling=None, works
     no adapter): one shared 4-bit projection and stacked adapters lora_A [L, R, K], lora_B [L, N, R] fp16, ids [M]
     int32 and scaling [L] float32 (None: 1) on the device. The workspace (uint8, w4a16_lora_workspace_size(M, R)
     bytes) is allocated here when not given."""
-    import torch
-    half = torch.float16
-    device, M, K = _rows_operand("A", A, half)
+    return _launch(_lora_gemm, "A", A, stream, wt, S, N, G, lora_A, lora_B, ids, scaling, workspace, out)
+
+
+def _lora_gemm(A, device, st, wt, S, N, G, lora_A, lora_B, ids, scaling, workspace, out):
+    M, K = A.shape
+    half = A.dtype
     if lora_A.dim() != 3:
         raise ValueError(f"lora_A must be [L, R, K], got {list(lora_A.shape)}")
-    L, R = lora_A.shape[0], lora_A.shape[1]
-    with _launch_on(device, stream) as st:
-        A = A if A.is_contiguous() else A.contiguous()
-        S = _scales("wt", wt, S, K, N, G, half, device)
-        lora_A = _operand("lora_A", lora_A, half, (L, R, K), device)
-        lora_B = _operand("lora_B", lora_B, half, (L, N, R), device)
-        ids = _operand("ids", ids, torch.int32, (M,), device)
-        if scaling is not None:
-            scaling = _operand("scaling", scaling, torch.float32, (L,), device)
-        C = _output("out", out, (M, N), A)
-        if M:
-            lib = _lib or load()
-            need = lib.w4a16_lora_workspace_size(M, R)
-            if workspace is None:
-                workspace = A.new_empty(max(need, 2) // 2)  # (2-byte elements; the size is a multiple of 256)
-            elif workspace.get_device() != device or not workspace.is_contiguous():
+    L, R, _ = lora_A.shape
+    S = _scales("wt", wt, S, K, N, G, half, device)
+    lora_A = _operand("lora_A", lora_A, half, (L, R, K), device)
+    lora_B = _operand("lora_B", lora_B, half, (L, N, R), device)
+    ids = _operand("ids", ids, _torch.int32, (M,), device)
+    scale = None
+    if scaling is not None:
+        scaling = _operand("scaling", scaling, _torch.float32, (L,), device)
+        scale = scaling.data_ptr()
+    C = _output("out", out, (M, N), A)
+    if M:
+        if workspace is None:
+            size = _lib.w4a16_lora_workspace_size(M, R)
+            workspace = A.new_empty(size // 2 if size > 0 else 1)  # (2-byte elements; a multiple of 256 bytes)
+        else:
+            size = workspace.numel() * workspace.element_size()
+            if workspace.get_device() != device or not workspace.is_contiguous():
                 raise ValueError(f"the workspace must be a dense tensor on {A.device}")
-            rc = lib.w4a16_lora_gemm(A.data_ptr(), wt.data_ptr(), S.data_ptr(), lora_A.data_ptr(), lora_B.data_ptr(),
-                                     ids.data_ptr(), None if scaling is None else scaling.data_ptr(), C.data_ptr(),
-                                     M, N, K, G, L, R, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), st)
-            if rc != OK:
-                raise W4A16Error(rc, "w4a16_lora_gemm")
+        rc = _lib.w4a16_lora_gemm(A.data_ptr(), wt.data_ptr(), S.data_ptr(), lora_A.data_ptr(), lora_B.data_ptr(),
+                                  ids.data_ptr(), scale, C.data_ptr(), M, N, K, G, L, R, workspace.data_ptr(), size,
+                                  st)
+        if rc != OK:
+            raise W4A16Error(rc, "w4a16_lora_gemm")
     return C
 
 
