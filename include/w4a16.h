@@ -357,7 +357,8 @@ int w4a16_gated_gemm_backward(const w4a16_half* dH_dev, const w4a16_half* Pg_dev
  * adapter that the row does not use.
  * R a multiple of 8 up to W4A16_MAX_RANK, 1 <= L < 2^31. workspace_dev:
  * w4a16_lora_workspace_size(M, R) bytes, caller-owned, not initialised; calls
- * that may overlap on the GPU must not share it. A, Wt, S, LA, LB and the
+ * that may overlap on the GPU must not share it, and neither it nor C may overlap
+ * an input. A, Wt, S, LA, LB and the
  * workspace 16-byte aligned, ids and scaling 4-byte, C 2-byte; contract of
  * w4a16_gemm otherwise. M == 0 is a no-op. Errors: INVALID_ARG (also a workspace
  * that is too small), MISALIGNED, UNSUPPORTED, CUDA. */
@@ -500,8 +501,9 @@ int w4a16_autotune(const w4a16_half* A_dev, const uint8_t* const* Wt, const w4a1
                    int32_t* best_tactic, float* best_us, float* times_us, int32_t times_capacity, void* stream);
 
 /* Test aid for the failure path of the bounded device waits (no counterpart
- * on the plugin pages). For every later launch of the tensor-core GEMM kernel
- * (w4a16_gemm with M > 16, and w4a16_grouped_gemm) until it is called again:
+ * on the plugin pages). For every later launch of the tensor-core kernels
+ * (w4a16_gemm, w4a16_gated_gemm and w4a16_lora_gemm with M > 16, w4a16_grouped_gemm,
+ * w4a16_gemm_dgrad, w4a16_gated_gemm_backward) until it is called again:
  * every bounded wait in the kernel runs out after wait_limit_cycles SM clock
  * cycles (<= 0 restores the default of about 2 s), and, if stall_stage >= 0,
  * the dequantising warps withhold the ready signal of that 64-deep K stage
@@ -515,7 +517,8 @@ int w4a16_set_fault_injection(int64_t stall_stage, int64_t wait_limit_cycles);
 
 /* Reads (and, if clear != 0, resets) the current device's status word. This
  * synchronizes the current device. Returns W4A16_OK, W4A16_ERR_TIMEOUT,
- * W4A16_ERR_BAD_OFFSETS, or W4A16_ERR_CUDA if the read itself failed. */
+ * W4A16_ERR_BAD_OFFSETS, W4A16_ERR_BAD_ROUTING, W4A16_ERR_BAD_ADAPTER, or
+ * W4A16_ERR_CUDA if the read itself failed. */
 int w4a16_device_status(int clear);
 
 #ifdef __cplusplus

@@ -83,23 +83,12 @@ struct DecodeParams {
 
 __device__ int g_decode_status;  // latched device-side error (0 = none)
 
-// 16 bytes of codes, read once: past L1.
-__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
+// 16 bytes of codes, read once, without a place in L1.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
-    return v;
-}
-
-// A scale: through L1, or past it (see the adapter form's early reads).
-template <bool PAST_L1>
-__device__ __forceinline__ uint16_t ld_scale(const void* p) {
-    uint16_t v;
-    if constexpr (PAST_L1)
-        asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    else
-        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 
@@ -147,6 +136,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
     const uint8_t* sb = LORA ? sa : reinterpret_cast<const uint8_t*>(p.sc[1]);
     const int blocks = active && kh < p.KB ? (p.KB - kh + p.KS - 1) / p.KS : 0;  // this warp's
     int to_load = blocks;
+    constexpr bool early = LORA;  // (its loads are not behind the dependency wait)
     auto load = [&](Block& x) {
         if (to_load > 0) {  // (the same for the whole warp)
             --to_load;
@@ -154,14 +144,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4a16_decode_kernel(const _
             // reads the block's first tile, with scales of zero.
             const bool missing = k_next >= static_cast<uint32_t>(p.KT) * 64u;
             const uint32_t off = missing ? w_off - 4096u : w_off;
-            x.a = ld_stream_v4(wa + off);
-            x.b = ld_stream_v4(wb + off);
+            x.a = early ? ld_cg_v4(wa + off) : ld_once_v4(wa + off);
+            x.b = early ? ld_cg_v4(wb + off) : ld_once_v4(wb + off);
 #pragma unroll
             for (int q = 0; q < kNS; ++q) {
                 const uint32_t gi = min(__umulhi(k_next + 16 * q, p.g_magic), static_cast<uint32_t>(p.ngroups - 1));
                 const uint32_t so = gi * row_step + s_off;
-                x.sa[q] = ld_scale<LORA>(sa + so);
-                x.sb[q] = ld_scale<LORA>(sb + (so + sb_more));
+                x.sa[q] = early ? ld_cg_u16(sa + so) : ld_u16(sa + so);
+                x.sb[q] = early ? ld_cg_u16(sb + (so + sb_more)) : ld_u16(sb + (so + sb_more));
                 if (missing) x.sa[q] = x.sb[q] = 0;
             }
             w_off += w_step;

@@ -182,11 +182,12 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
         const int i = ib + li;
         if constexpr (GATED) {
             if (li < nst) {
-                c[0] = ld_nc_v4(gw + static_cast<int64_t>(i) * kTile);
-                c[1] = ld_nc_v4(gw + static_cast<int64_t>(i) * kTile + 2048);
+                c[0] = ld_cg_v4(gw + static_cast<int64_t>(i) * kTile);
+                c[1] = ld_cg_v4(gw + static_cast<int64_t>(i) * kTile + 2048);
 #pragma unroll
                 for (int q = 0; q < kScales; ++q)
-                    sv[q] = __ldg(gs + static_cast<int64_t>(min((i * kDepth + 16 * q) / p.G, p.ngroups - 1)) * p.N);
+                    sv[q] = __ushort_as_half(
+                        ld_cg_u16(gs + static_cast<int64_t>(min((i * kDepth + 16 * q) / p.G, p.ngroups - 1)) * p.N));
             }
             li += kTurn;
             return;
@@ -196,10 +197,10 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
         const int n = ns * kDepth + r;
         if (li < nst && kt_ok && n < p.N) {
             const uint8_t* w = p.wt[src] + (static_cast<int64_t>(ns >> 1) * p.KT + kt) * kTile + ((ns & 1) * 64 + r) * 16;
-            c[0] = ld_nc_v4(w);
-            c[1] = ld_nc_v4(w + 2048);
+            c[0] = ld_cg_v4(w);
+            c[1] = ld_cg_v4(w + 2048);
 #pragma unroll
-            for (int q = 0; q < kScales; ++q) sv[q] = __ldg(p.sc[src] + soff[q] + n);
+            for (int q = 0; q < kScales; ++q) sv[q] = __ushort_as_half(ld_cg_u16(p.sc[src] + soff[q] + n));
         } else {
             // Past N the weights must be exact zeros: they meet the gradient's zero
             // fill, and a clamped scale could be an infinity.
@@ -502,15 +503,15 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
 constexpr int kSlopeThreads = 256;
 
 __global__ void __launch_bounds__(kSlopeThreads)
-    gated_slopes_kernel(const __half* __restrict__ dH, const __half* __restrict__ g, const __half* __restrict__ u,
-                        __half* __restrict__ dG, __half* __restrict__ dU, int64_t vecs, int act) {
+    gated_slopes_kernel(const __half* dH, const __half* g, const __half* u, __half* dG, __half* dU, int64_t vecs,
+                        int act) {
     grid_dependency_wait();  // the inputs come from the previous kernels
     grid_launch_dependents();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSlopeThreads + threadIdx.x; i < vecs;
          i += static_cast<int64_t>(gridDim.x) * kSlopeThreads) {
-        const uint4 vh = reinterpret_cast<const uint4*>(dH)[i];
-        const uint4 vg = reinterpret_cast<const uint4*>(g)[i];
-        const uint4 vu = reinterpret_cast<const uint4*>(u)[i];
+        const uint4 vh = ld_v4(dH + 8 * i);
+        const uint4 vg = ld_v4(g + 8 * i);
+        const uint4 vu = ld_v4(u + 8 * i);
         uint4 og, ou;
         const __half2* h2 = reinterpret_cast<const __half2*>(&vh);
         const __half2* g2 = reinterpret_cast<const __half2*>(&vg);
@@ -631,6 +632,9 @@ int64_t wide_cost(int64_t M, int64_t blocks, int64_t km, int64_t sms, int64_t* m
     return best;
 }
 
+// The grid's limits: at most 65535 output blocks and row tiles of the launch forms below.
+bool dgrad_grid_fits(int64_t M, int64_t K) { return K <= 65535 * int64_t(kOutK) && M <= 65533 * int64_t(256); }
+
 // dA = sum over the sources of dC_i x W_i^T.
 int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, const w4a16_half* const* S,
           w4a16_half* dA, int64_t M, int64_t N, int64_t K, int64_t G, cudaStream_t stream) {
@@ -650,7 +654,7 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
     const int64_t tile_rows = rows_of_tile(M, MT);
     const DgradVariant& v = kDgrad[vi];
     const int64_t KB = (K + kOutK * v.km - 1) / (kOutK * v.km);
-    if (KB > 65535 || MT > 65535) return W4A16_ERR_UNSUPPORTED;
+    if (!dgrad_grid_fits(M, K)) return W4A16_ERR_UNSUPPORTED;
     DgradParams p;
     std::memset(&p, 0, sizeof(p));
     for (int i = 0; i < 2; ++i) {
@@ -835,6 +839,7 @@ extern "C" int w4a16_gated_gemm_backward(const w4a16_half* dH_dev, const w4a16_h
     if (M == 0) return W4A16_OK;
     rc = check_device();
     if (rc) return rc;
+    if (!dgrad_grid_fits(M, K)) return W4A16_ERR_UNSUPPORTED;  // (before the slopes are enqueued)
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     rc = gated_slopes(dH_dev, Pg_dev, Pu_dev, dPg_dev, dPu_dev, M * N, act, s);
     if (rc) return rc;

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
     // (Adapter form: weights, scales and activations are read past L1 without waiting
     // for the kernel that makes V, which lets this one start only once everything
     // before it is complete; see the wait before the adapter stages.)
-    auto load_scale = [](const __half* q) { return LORA ? __ldcg(q) : __ldg(q); };
+    auto load_scale = [](const __half* q) { return FORM == kPlain ? __ldg(q) : __ldcg(q); };
     int li = grp;
     int kk = (kb + grp) * kTileK;
     int gk = kk / p.G;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(threads_for(DQ), MINB)
             const uint8_t* src = wcol + static_cast<int64_t>(kb + li) * kTileBytes;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-                r[c] = LORA ? __ldcg(reinterpret_cast<const uint4*>(src + c * 2048)) : ld_nc_v4(src + c * 2048);
+                r[c] = FORM == kPlain ? ld_nc_v4(src + c * 2048) : ld_cg_v4(src + c * 2048);
             if constexpr (OG) {
                 sv[0] = load_scale(scol + static_cast<int64_t>(min(gk, p.ngroups - 1)) * p.N);
             } else {

@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(W * 32) lora_down_kernel(const DownParams p) {
             for (int u = 0; u < kBatch; ++u) {
                 const int k = k0 + 32 * kWarps * u;
                 const int kk = k + 8 * t < p.K ? k : -8 * t;
-                x0[u] = ld_nc_v4(a0 + kk);
-                x1[u] = ld_nc_v4(a1 + kk);
+                x0[u] = ld_v4(a0 + kk);
+                x1[u] = ld_v4(a1 + kk);
 #pragma unroll
-                for (int j = 0; j < RT; ++j) y[u][j] = ld_nc_v4(lb[j] + kk);
+                for (int j = 0; j < RT; ++j) y[u][j] = ld_v4(lb[j] + kk);
             }
             __syncwarp();  // (keeps the loads together: the compiler would move each down to its MMA)
 #pragma unroll
