@@ -213,3 +213,27 @@ def test_two_blocks_per_cta(M, K, N, G):
     ref, err = f.product(dC, layer.W.T)
     assert f.worst(dA.cpu().numpy(), ref, f.half_step(ref) + 1.001 * err) <= 1
     assert guards_intact(flat, pad, M * K)
+
+
+def test_calls_on_two_streams_at_once():
+    # forms that fill tensor memory, forms that share it and cluster splits, side by side on two streams
+    shapes = [(300, 1112, 2856, 64), (40, 512, 1024, 64), (20, 264, 2048, 128), (600, 2048, 4104, 128), (5, 1024, 2048, 64)]
+    calls = []
+    for i, (M, K, N, G) in enumerate(shapes):
+        gate, up = Layer(K, N, G, seed=i), Layer(K, N, G, seed=i + 50)
+        A, dC = dev(workloads.dense(M, K, N, G, i).A), dev(gradient(M, N, i))
+        calls.append(lambda a=A, g=gate, u=up, s=None: w.gated_gemm(a, g.wt, g.S, u.wt, u.S, g.N, g.G, stream=s))
+        calls.append(lambda d=dC, g=gate, s=None: w.gemm_dgrad(d, g.wt, g.S, g.K, g.G, stream=s))
+    refs = [c() for c in calls]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for r in range(3):
+        for i in range(len(calls)):
+            for x in (0, 1):  # the other stream runs the list from its other end
+                j = i if x == 0 else len(calls) - 1 - i
+                got[x].append((j, calls[j](s=sides[x])))
+    torch.cuda.synchronize()
+    for lists in got:
+        for j, out in lists:
+            assert torch.equal(out, refs[j]), j
