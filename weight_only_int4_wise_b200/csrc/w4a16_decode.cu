@@ -3,10 +3,9 @@
 // w4a16_lora_gemm; the Int4GroupwiseGemmPluginV2 page describes the plain product
 // that both contain).
 //
-// Bound by streaming the codes, and close to it by decoding them: an SM must
-// decode about 21 bytes (42 weights) per clock to keep up with HBM. So the
-// kernel is laid out around the instructions per weight and an even share of the
-// weights per SM:
+// The floor is the stream of the codes: to keep up with HBM an SM would have to
+// decode about 21 bytes (42 weights) per clock. So the kernel is laid out around
+// the instructions per weight and an even share of the weights per SM:
 //   - one CTA per SM; a warp owns 16 rows of the MMA's A operand (weights: 8 gate
 //     and the same 8 up columns, or 16 columns of the plain product) for every
 //     KS-th 128-deep block of K, a CTA P such warp tiles times KS warps each, with P
