@@ -301,9 +301,10 @@ int64_t w4a16_moe_static_scratch_bytes(void);
 /* Gated projections: H_dev [M, N] = fp16(act(A W_gate) * (A W_up)) from
  * activations A_dev [M, K] and two weight matrices [K -> N] of one group size
  * G. Both products, the activation (any W4A16_ACT_*, SILU included) and their
- * product are fp32; H is rounded once. If Pg_dev and Pu_dev are given (both or
- * neither), the projections themselves are also written, Pg_dev = fp16(A W_gate)
- * and Pu_dev = fp16(A W_up), both [M, N]: what w4a16_gated_gemm_backward reads.
+ * product are fp32; H is rounded once. A NaN projection makes its element of H
+ * NaN under every activation, ReLU included. If Pg_dev and Pu_dev are given
+ * (both or neither), the projections themselves are also written, Pg_dev =
+ * fp16(A W_gate) and Pu_dev = fp16(A W_up), both [M, N]: what w4a16_gated_gemm_backward reads.
  * flags: 0 or W4A16_FLAG_STATIC_WEIGHTS (as for w4a16_gemm_ex; it covers both
  * weight matrices). Contract of w4a16_gemm otherwise; H, Pg and Pu 2-byte
  * aligned, and none of the outputs may overlap A or another output. M == 0 is a
@@ -329,9 +330,10 @@ int w4a16_gemm_dgrad(const w4a16_half* dC_dev, const uint8_t* Wt_dev, const w4a1
  *     dA  = fp16(dPg W_gate^T + dPu W_up^T)      (one fp32 sum over both),
  * all three written: dPg_dev and dPu_dev [M, N] are what gradients of adapters
  * on the projections need, dA_dev [M, K] goes on to the layer below. relu'(0) =
- * 0. No output may overlap an input or another output. All [M, N] matrices,
- * weights and scales 16-byte aligned, dA 2-byte aligned; flags and the rest as
- * for w4a16_gated_gemm. Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, CUDA. */
+ * 0; a NaN in Pg makes dPu NaN, and dPg too unless act is IDENTITY. No output
+ * may overlap an input or another output. All [M, N] matrices, weights and
+ * scales 16-byte aligned, dA 2-byte aligned; flags and the rest as for
+ * w4a16_gated_gemm. Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, CUDA. */
 int w4a16_gated_gemm_backward(const w4a16_half* dH_dev, const w4a16_half* Pg_dev, const w4a16_half* Pu_dev,
                               const uint8_t* Wt_gate_dev, const w4a16_half* S_gate_dev, const uint8_t* Wt_up_dev,
                               const w4a16_half* S_up_dev, w4a16_half* dPg_dev, w4a16_half* dPu_dev,

@@ -1,0 +1,69 @@
+"""The operators on frozen 4-bit weights where the ordinary cases cannot see a mistake: NaN gates."""
+import numpy as np
+import pytest
+import torch
+
+import frozen_util as f
+import workloads
+import weight_only_int4_wise_b200 as w
+from gpu_util import dev, device_weights, guarded_output, guards_intact
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    w.device_status(clear=True)
+    yield
+    assert w.device_status(clear=True) == w.OK
+
+
+class Layer:
+    def __init__(self, K, N, G, seed, scale=1.0):
+        c = workloads.dense(1, K, N, G, seed)
+        self.K, self.N, self.G = K, N, G
+        self.S64 = (c.S.astype(np.float64) * scale).astype(np.float16)
+        self.S, self.W = dev(self.S64), f.matrix(c.q, self.S64, G)
+        self.wt = device_weights(c.q)[1]
+
+
+def normal(shape, seed, scale=1.0):
+    return (np.random.Generator(np.random.PCG64(seed)).standard_normal(shape) * scale).astype(np.float16)
+
+
+def gated(A, gate, up, act=w.ACT_SILU, **kw):
+    return w.gated_gemm(A, gate.wt, gate.S, up.wt, up.S, gate.N, gate.G, act, **kw)
+
+
+# ---------------------------------------------------------------- NaN gates
+
+
+@pytest.mark.parametrize("act", range(5))
+@pytest.mark.parametrize("M,K,N", [(3, 128, 136), (16, 128, 136), (40, 512, 136), (300, 256, 136), (300, 136, 8968)])
+def test_a_nan_gate_is_not_lost_forward(M, K, N, act):
+    # one column of the gate has a NaN scale, the up projection is finite: the column of H is NaN whatever the activation
+    gate, up = Layer(K, N, 64, 1), Layer(K, N, 64, 2)
+    A = dev(normal((M, K), 3))
+    clean = gated(A, gate, up, act)
+    gate.S[0, 5] = float("nan")
+    H, g, _ = gated(A, gate, up, act, save=True)
+    rest = [n for n in range(N) if n != 5]
+    assert torch.isnan(H[:, 5]).all() and torch.isnan(g[:, 5]).all()
+    assert torch.equal(H[:, rest], clean[:, rest]) and torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("act", range(5))
+def test_a_nan_gate_is_not_lost_backward(act):
+    M, K, N, G = 6, 64, 72, 64
+    gate, up = Layer(K, N, G, 1), Layer(K, N, G, 2)
+    g, u, dH = dev(normal((M, N), 1)), dev(normal((M, N), 2)), dev(normal((M, N), 3, 0.05))
+    call = lambda: w.gated_gemm_backward(dH, g, u, gate.wt, gate.S, up.wt, up.S, K, G, act)
+    clean = call()
+    g[2, 9] = float("nan")
+    dA, dG, dU = call()
+    assert torch.isnan(dU[2, 9]) and torch.isnan(dA[2]).all()
+    assert torch.isnan(dG[2, 9]) or act == w.ACT_IDENTITY  # (the identity's slope is 1 everywhere)
+    rows, cols = [m for m in range(M) if m != 2], [n for n in range(N) if n != 9]
+    assert torch.equal(dA[rows], clean[0][rows])
+    for got, ref in ((dG, clean[1]), (dU, clean[2])):
+        assert torch.equal(got[rows], ref[rows]) and torch.equal(got[:, cols], ref[:, cols])

@@ -51,7 +51,7 @@ __device__ __forceinline__ float gate_value(float x, int act) {
         case W4A16_ACT_SILU: return x * logistic(x);
         case W4A16_ACT_GELU_ERF: return 0.5f * x * erfcf(x * -kSqrtHalf);
         case W4A16_ACT_GELU_TANH: return x * logistic(kTanhScale * (x + 0.044715f * x * x * x));
-        case W4A16_ACT_RELU: return fmaxf(x, 0.f);
+        case W4A16_ACT_RELU: return x < 0.f ? 0.f : x;  // (fmaxf would turn a NaN into 0)
         default: return x;
     }
 }
@@ -75,8 +75,8 @@ __device__ __forceinline__ float gate_slope(float x, int act, float* v) {
             return fmaf(x * t * (1.f - t), kTanhScale * (1.f + 0.134145f * x * x), t);
         }
         case W4A16_ACT_RELU:
-            *v = fmaxf(x, 0.f);
-            return x > 0.f ? 1.f : 0.f;
+            *v = x < 0.f ? 0.f : x;
+            return x > 0.f ? 1.f : (x <= 0.f ? 0.f : x);  // (a NaN's slope is that NaN, as for the other activations)
         default:
             *v = x;
             return 1.f;
