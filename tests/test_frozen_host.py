@@ -1,0 +1,46 @@
+"""Host code of the operators on frozen 4-bit weights that needs no GPU: small programs compiled against the library's
+own headers."""
+import os
+import subprocess
+import textwrap
+
+from weight_only_int4_wise_b200 import build
+
+
+def compile_and_run(tmp_path, name, source, flags=()):
+    """Compiles a C++ program that includes headers of csrc/ and returns its completed run."""
+    cpp, exe = os.path.join(tmp_path, name + ".cpp"), os.path.join(tmp_path, name)
+    with open(cpp, "w") as out:
+        out.write(textwrap.dedent(source))
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", build.CSRC, *flags, cpp, "-o", exe, "-pthread"],
+                   check=True)
+    return subprocess.run([exe], capture_output=True, text=True, timeout=120)
+
+
+def test_every_warp_indexes_inside_the_parameter_arrays(tmp_path):
+    # The set-up of the transposed and wide gated products runs on all warps, the producer's and the MMA issuer's too:
+    # the block that indexes the arrays of two weight matrices is 0 or 1 for each, and the groups share out all stages.
+    run = compile_and_run(tmp_path, "roles", """
+        #include <cstdio>
+        #include "roles.h"
+        int main() {
+            const int forms[][2] = {{1, 2}, {1, 4}, {2, 4}};  // blocks per CTA, decoding groups
+            for (auto& form : forms) {
+                const int km = form[0], groups = form[1], turn = groups / km;
+                int taken[2][4] = {};
+                for (int warp = 0; warp < w4a16::kFirstDecodeWarp + w4a16::kGroupWarps * groups; ++warp) {
+                    const int block = w4a16::block_of_warp(warp, km), stage = w4a16::stage_of_warp(warp, km);
+                    if (block < 0 || block >= km || stage < 0 || stage >= turn) {
+                        std::printf("warp %d of (%d, %d): block %d, stage %d\\n", warp, km, groups, block, stage);
+                        return 1;
+                    }
+                    if (warp >= w4a16::kFirstDecodeWarp) ++taken[block][stage];
+                }
+                for (int b = 0; b < km; ++b)
+                    for (int s = 0; s < turn; ++s)
+                        if (taken[b][s] != w4a16::kGroupWarps) return 2;
+            }
+            return 0;
+        }
+    """)
+    assert run.returncode == 0, run.stdout

@@ -56,6 +56,7 @@
 #include "dequant.cuh"
 #include "epilogue.cuh"
 #include "ptx.cuh"
+#include "roles.h"
 #include "w4a16_internal.h"
 #include "waits.cuh"
 
@@ -69,7 +70,6 @@ constexpr int kOutK = 128;         // k per CTA (MMA M)
 constexpr int kDepth = 64;         // contraction per stage
 constexpr int kTile = 4096;        // bytes of one 128-column x 64-row code tile
 constexpr int kABytes = kOutK * kDepth * 2;
-constexpr int kGroupWarps = 4;
 constexpr int kPrefetchStages = 12;  // code tiles the producer pulls into L2 ahead of use
 
 __host__ __device__ constexpr int dgrad_threads(int dq) { return (2 + kGroupWarps * dq) * 32; }
@@ -158,10 +158,10 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
     const int n_mma = min(BN, (rows + 15) & ~15);
 
     // ---- decoding threads' state; the first loads go out before the setup below
-    const int dw = warp - 2;
-    const int kb = (dw >> 2) % KM;   // which of the CTA's blocks of k this group decodes
-    const int grp = (dw >> 2) / KM;  // its first stage
-    const int kblk = GATED ? blockIdx.y : blockIdx.y * KM + (warp >= 2 ? kb : 0);  // block of the output
+    const int dw = warp - kFirstDecodeWarp;
+    const int kb = block_of_warp(warp, KM);   // which of the CTA's blocks of k this group decodes
+    const int grp = stage_of_warp(warp, KM);  // its first stage
+    const int kblk = GATED ? blockIdx.y : blockIdx.y * KM + kb;  // block of the output
     const int t = static_cast<int>(threadIdx.x - 64) & 127;  // thread inside its group
     // Transposed: column r of the stage (contraction index) and 64 of the block's 128 k.
     // Gated: column t of the block's 128, the stage's 64 k.
