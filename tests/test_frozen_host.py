@@ -44,3 +44,42 @@ def test_every_warp_indexes_inside_the_parameter_arrays(tmp_path):
         }
     """)
     assert run.returncode == 0, run.stdout
+
+
+def test_threads_that_make_first_calls_at_once_do_not_race(tmp_path):
+    # Under the race detector: eight threads prepare two devices at once; each device is prepared once, a failure is
+    # tried again, and what the preparation wrote is there for every thread that finds it done.
+    run = compile_and_run(tmp_path, "once", """
+        #include <cstdio>
+        #include <thread>
+        #include <vector>
+        #include "once.h"
+        static w4a16::OncePerDevice once;
+        static int tries[2], prepared[2];  // plain: the class has to order them
+        int main() {
+            std::vector<std::thread> threads;
+            std::atomic<int> wrong{0};
+            for (int t = 0; t < 8; ++t)
+                threads.emplace_back([t, &wrong] {
+                    const int dev = t & 1;
+                    for (int i = 0; i < 1000; ++i) {
+                        const int rc = once.run(dev, [dev] {
+                            if (++tries[dev] == 1) return 3;
+                            prepared[dev] += 1;
+                            return 0;
+                        });
+                        if (rc == 0 && prepared[dev] != 1) wrong.fetch_add(1);
+                        if (rc != 0 && rc != 3) wrong.fetch_add(1);
+                    }
+                });
+            for (auto& t : threads) t.join();
+            return wrong.load() || tries[0] != 2 || tries[1] != 2;
+        }
+    """, flags=("-fsanitize=thread",))
+    assert run.returncode == 0, run.stdout + run.stderr
+
+
+def test_no_launch_keeps_an_unguarded_table():
+    for path in build.sources():
+        with open(path) as source:
+            assert "attr_done" not in source.read(), path

@@ -45,6 +45,7 @@
 #include "../../include/w4a16.h"
 #include "dequant.cuh"
 #include "epilogue.cuh"
+#include "once.h"
 #include "ptx.cuh"
 #include "w4a16_internal.h"
 #include "waits.cuh"
@@ -374,20 +375,20 @@ int decode_launch(DecodeParams& p, DecodeForm form, int64_t M, int64_t N, int64_
         w4a16_decode_kernel<2, kGated, false>, w4a16_decode_kernel<2, kGated, true>,
         w4a16_decode_kernel<1, kLora, false>,  w4a16_decode_kernel<1, kLora, true>,
         w4a16_decode_kernel<2, kLora, false>,  w4a16_decode_kernel<2, kLora, true>};
-    static bool attr_done[8][64] = {};
+    static OncePerDevice prepared[8];
     const int mt = M <= 8 ? 1 : 2;
     const int vi = 4 * form + 2 * (mt - 1) + (G % 32 ? 1 : 0);
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
-    if (!attr_done[vi][dev]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
-                                 cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
-                cudaSuccess)
-            return W4A16_ERR_CUDA;
-        attr_done[vi][dev] = true;
-    }
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return W4A16_ERR_CUDA;
+    const int rc = prepared[vi].run(dev, [&] {
+        const void* fn = reinterpret_cast<const void*>(kernels[vi]);
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess &&
+                       cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                            cudaSharedmemCarveoutMaxShared) == cudaSuccess
+                   ? W4A16_OK
+                   : W4A16_ERR_CUDA;
+    });
+    if (rc) return rc;
     p.M = static_cast<int32_t>(M);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);

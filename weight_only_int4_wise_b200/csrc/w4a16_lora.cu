@@ -32,6 +32,7 @@
 #include <cstdint>
 
 #include "../../include/w4a16.h"
+#include "once.h"
 #include "ptx.cuh"
 #include "w4a16_internal.h"
 
@@ -231,16 +232,17 @@ int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
 
 template <int RT, int W>
 int launch_down(const DownParams& p, dim3 grid, cudaStream_t stream) {
-    static bool attr_done[64] = {};
+    static OncePerDevice prepared;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
-    if (!attr_done[dev]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(&lora_down_kernel<RT, W>),
-                                 cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-            return W4A16_ERR_CUDA;
-        attr_done[dev] = true;
-    }
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return W4A16_ERR_CUDA;
+    const int rc = prepared.run(dev, [] {
+        return cudaFuncSetAttribute(reinterpret_cast<const void*>(&lora_down_kernel<RT, W>),
+                                    cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared) == cudaSuccess
+                   ? W4A16_OK
+                   : W4A16_ERR_CUDA;
+    });
+    if (rc) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(W * 32, 1, 1);

@@ -33,6 +33,7 @@
 #include <cstdint>
 
 #include "../../include/w4a16.h"
+#include "once.h"
 #include "ptx.cuh"
 #include "w4a16_internal.h"
 
@@ -293,17 +294,18 @@ int quantize_launch(const w4a16_half* W_dev, void* out_dev, w4a16_half* S_dev, i
     CUtensorMap map;
     if (tma && make_half_map_2d(&map, W_dev, static_cast<uint64_t>(N), static_cast<uint64_t>(K),
                                 static_cast<uint64_t>(N) * 2, kTileCols, static_cast<uint32_t>(G)) == W4A16_OK) {
-        static bool attr_done[64] = {};
+        static OncePerDevice prepared;
         int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return W4A16_ERR_CUDA;
         const size_t smem = 128 + kSlices * kQuantThreads * 8 + static_cast<size_t>(kMaxTmaGroup) * kTileCols * 2;
-        if (!attr_done[dev]) {
-            if (cudaFuncSetAttribute(reinterpret_cast<const void*>(quantize_tma_kernel<BITS>),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-                cudaSuccess)
-                return W4A16_ERR_CUDA;
-            attr_done[dev] = true;
-        }
+        rc = prepared.run(dev, [&] {
+            return cudaFuncSetAttribute(reinterpret_cast<const void*>(quantize_tma_kernel<BITS>),
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(smem)) == cudaSuccess
+                       ? W4A16_OK
+                       : W4A16_ERR_CUDA;
+        });
+        if (rc) return rc;
         quantize_tma_kernel<BITS><<<grid, kQuantThreads * kSlices,
                                     128 + kSlices * kQuantThreads * 8 + static_cast<size_t>(G) * kTileCols * 2, st>>>(
             map, reinterpret_cast<uint16_t*>(out_dev), reinterpret_cast<__half2*>(S_dev), K, N, G, groups);

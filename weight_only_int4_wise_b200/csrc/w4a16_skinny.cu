@@ -33,6 +33,7 @@
 #include "../../include/w4a16.h"
 #include "dequant.cuh"
 #include "epilogue.cuh"
+#include "once.h"
 #include "ptx.cuh"
 #include "w4a16_internal.h"
 
@@ -502,9 +503,9 @@ namespace {
 // Launch with filled parameters; grid z = 1 (dense) or the number of experts.
 int skinny_launch_params(const SkinnyPlan& plan, SkinnyParams& p, int64_t N, int64_t K, int64_t G, unsigned grid_z,
                          cudaStream_t stream) {
-    static bool attr_done[12][64] = {};
+    static OncePerDevice prepared[12];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return W4A16_ERR_CUDA;
     const int kh = plan.threads / kSkThreads;
     const int vi = (p.grouped ? 6 : 0) + (plan.mt == 2 ? 4 : (kh == 2 ? 2 : 0)) + (plan.depth == 8 / kh ? 1 : 0);
     // (shared-memory carve-out: the largest, so two CTAs fit per SM)
@@ -515,15 +516,15 @@ int skinny_launch_params(const SkinnyPlan& plan, SkinnyParams& p, int64_t N, int
         w4a16_skinny_kernel<1, 4, 1, true>,  w4a16_skinny_kernel<1, 8, 1, true>,
         w4a16_skinny_kernel<1, 2, 2, true>,  w4a16_skinny_kernel<1, 4, 2, true>,
         w4a16_skinny_kernel<2, 4, 1, true>,  w4a16_skinny_kernel<2, 8, 1, true>};
-    if (!attr_done[vi][dev]) {
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess ||
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(kernels[vi]),
-                                 cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
-                cudaSuccess)
-            return W4A16_ERR_CUDA;
-        attr_done[vi][dev] = true;
-    }
+    const int rc = prepared[vi].run(dev, [&] {
+        const void* fn = reinterpret_cast<const void*>(kernels[vi]);
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) == cudaSuccess &&
+                       cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                            cudaSharedmemCarveoutMaxShared) == cudaSuccess
+                   ? W4A16_OK
+                   : W4A16_ERR_CUDA;
+    });
+    if (rc) return rc;
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.G = static_cast<int32_t>(G);
