@@ -1,4 +1,5 @@
-"""The operators on frozen 4-bit weights where the ordinary cases cannot see a mistake: NaN gates."""
+"""The operators on frozen 4-bit weights where the ordinary cases cannot see a mistake: NaN gates, and waits that run
+out."""
 import numpy as np
 import pytest
 import torch
@@ -67,3 +68,26 @@ def test_a_nan_gate_is_not_lost_backward(act):
     assert torch.equal(dA[rows], clean[0][rows])
     for got, ref in ((dG, clean[1]), (dU, clean[2])):
         assert torch.equal(got[rows], ref[rows]) and torch.equal(got[:, cols], ref[:, cols])
+
+
+# ---------------------------------------------------------------- waits that run out
+
+
+def test_transposed_stall_stage_counts_from_each_ranks_range():
+    # 16 stages over a cluster of two: no rank has a stage 8 of its own, both have a stage 7
+    layer = Layer(256, 1024, 64, 0)
+    dC = normal((20, 1024), 1, 0.05)
+    ref, err = f.product(dC, layer.W.T)
+    for stage, status in ((8, w.OK), (7, w.ERR_TIMEOUT)):
+        out = torch.full((20, 256), 7.0, dtype=torch.float16, device="cuda")
+        try:
+            w.w4a16_set_fault_injection(stage, 2_000_000)
+            w.gemm_dgrad(dev(dC), layer.wt, layer.S, 256, 64, out=out)
+            torch.cuda.synchronize()
+        finally:
+            w.w4a16_set_fault_injection(-1, 0)
+        assert w.device_status(clear=True) == status
+        if status == w.OK:
+            assert f.worst(out.cpu().numpy(), ref, f.half_step(ref) + 1.001 * err) <= 1
+        else:
+            assert (out == 7.0).all()

@@ -90,7 +90,7 @@ struct DgradParams {
     int32_t prefetch;       // weights/scales may be read before the previous kernel finishes
     int32_t vec_out;        // output rows start on 16-byte boundaries
     long long wait_limit;
-    int32_t stall_stage;    // test aid: withhold this stage's ready signal (< 0: never)
+    int32_t stall_stage;    // test aid: withhold the ready signal of this stage of each CTA's range (< 0: never)
 };
 
 template <int BN, int LB, int LA, int KM>
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(dgrad_threads(DQ), MINB)
                                                   p.wait_limit, &g_dgrad_status))
                 return false;
             __syncwarp();
-            if (lane == 0 && ib + l != p.stall_stage) mbar_arrive(&ready[sa]);
+            if (lane == 0 && l != p.stall_stage) mbar_arrive(&ready[sa]);
             return true;
         };
         // Two register slots, used alternately: codes stay in the registers they were loaded into.
