@@ -508,13 +508,16 @@ int w4a16_autotune(const w4a16_half* A_dev, const uint8_t* const* Wt, const w4a1
  * w4a16_gemm_dgrad, w4a16_gated_gemm_backward) until it is called again:
  * every bounded wait in the kernel runs out after wait_limit_cycles SM clock
  * cycles (<= 0 restores the default of about 2 s), and, if stall_stage >= 0,
- * the dequantising warps withhold the ready signal of that 64-deep K stage
- * (counted from the start of each CTA's K range), so the MMA thread's wait for
- * it runs out. The kernel then latches W4A16_ERR_TIMEOUT, lets every copy and
+ * the dequantising warps withhold the ready signal of that 64-deep stage
+ * (counted from the start of each CTA's range of the contraction), so the MMA
+ * thread's wait for it runs out. The kernel then latches W4A16_ERR_TIMEOUT, lets every copy and
  * MMA in flight complete, frees its tensor memory and writes no output tile
  * that the stalled stage (or, with K split over a cluster, any CTA of the
- * cluster) contributes to; nothing faults or hangs. Process-wide; always
- * returns W4A16_OK. */
+ * cluster) contributes to; nothing faults or hangs. The decode-sized forms of
+ * w4a16_gated_gemm and w4a16_lora_gemm (M <= 16) have one bounded wait, for
+ * their activations, under the same limit (stall_stage does not concern them):
+ * a CTA whose wait runs out latches W4A16_ERR_TIMEOUT, lets its copies land and
+ * writes none of its columns. Process-wide; always returns W4A16_OK. */
 int w4a16_set_fault_injection(int64_t stall_stage, int64_t wait_limit_cycles);
 
 /* Reads (and, if clear != 0, resets) the current device's status word. This

@@ -91,3 +91,63 @@ def test_transposed_stall_stage_counts_from_each_ranks_range():
             assert f.worst(out.cpu().numpy(), ref, f.half_step(ref) + 1.001 * err) <= 1
         else:
             assert (out == 7.0).all()
+
+
+class Adapters:
+    def __init__(self, layer, M, L, R, seed, la_scale=None):
+        self.layer = layer
+        self.LA = normal((L, R, layer.K), seed, la_scale or 1 / np.sqrt(layer.K))
+        self.LB = normal((L, layer.N, R), seed + 1, 0.1)
+        self.ids = (np.arange(M) % L).astype(np.int32)
+        self.scaling = np.linspace(0.5, 1.5, L).astype(np.float32)
+
+    def run(self, A, **kw):
+        x = self.layer
+        return w.lora_gemm(A, x.wt, x.S, x.N, x.G, dev(self.LA), dev(self.LB), dev(self.ids), dev(self.scaling), **kw)
+
+    def reference(self, A):
+        return f.lora(A, self.layer.W, self.LA, self.LB, self.ids, self.scaling)
+
+
+@pytest.mark.parametrize("M,K,N", [(40, 1024, 512), (130, 320, 264), (300, 1024, 520)])
+def test_adapter_product_with_a_stalled_stage_writes_nothing(M, K, N):
+    a = Adapters(Layer(K, N, 64, M), M, 5, 16, M)
+    A = normal((M, K), 9)
+    out = torch.full((M, N), 7.0, dtype=torch.float16, device="cuda")
+    try:
+        w.w4a16_set_fault_injection(0, 2_000_000)
+        a.run(dev(A), out=out)
+        torch.cuda.synchronize()
+    finally:
+        w.w4a16_set_fault_injection(-1, 0)
+    assert w.device_status(clear=True) == w.ERR_TIMEOUT
+    assert (out == 7.0).all()
+    ref, bound = a.reference(A)
+    assert f.worst(a.run(dev(A)).cpu().numpy(), ref, bound) <= 1
+
+
+@pytest.mark.parametrize("M", [1, 16])
+def test_decode_forms_with_a_short_wait_limit(M):
+    # the wait for the activations may or may not run out: each block of columns is right or untouched, and reported
+    K, N, G = 4096, 2056, 128
+    gate, up = Layer(K, N, G, 1), Layer(K, N, G, 2)
+    a = Adapters(gate, M, 3, 16, 5)
+    A = normal((M, K), 9)
+    (H, _, _), (eH, _, _) = f.gated(A, gate.W, up.W, w.ACT_SILU)
+    C, eC = a.reference(A)
+    for call, ref, bound in ((lambda **kw: gated(dev(A), gate, up, **kw), H, eH), (lambda **kw: a.run(dev(A), **kw), C, eC)):
+        out = torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
+        try:
+            w.w4a16_set_fault_injection(-1, 1)
+            call(out=out)
+            torch.cuda.synchronize()
+        finally:
+            w.w4a16_set_fault_injection(-1, 0)
+        status = w.device_status(clear=True)
+        got = out.cpu().numpy()
+        missing = np.isnan(got)
+        assert status == (w.ERR_TIMEOUT if missing.any() else status) and status in (w.OK, w.ERR_TIMEOUT)
+        blocks = missing.reshape(M, N // 8, 8)
+        assert (blocks == blocks[:1, :, :1]).all()  # whole columns in blocks of eight
+        assert np.all(np.abs(got.astype(np.float64) - ref)[~missing] <= bound[~missing])
+        assert f.worst(call().cpu().numpy(), ref, bound) <= 1
