@@ -1,9 +1,13 @@
 """Host code of the operators on frozen 4-bit weights that needs no GPU: small programs compiled against the library's
-own headers."""
+own headers, and refusals in front of any launch."""
 import os
 import subprocess
 import textwrap
 
+import pytest
+import torch
+
+import weight_only_int4_wise_b200 as w
 from weight_only_int4_wise_b200 import build
 
 
@@ -83,3 +87,11 @@ def test_no_launch_keeps_an_unguarded_table():
     for path in build.sources():
         with open(path) as source:
             assert "attr_done" not in source.read(), path
+
+
+def test_outputs_that_would_not_be_written_are_refused():
+    rows, wt, S = torch.zeros((4, 64)).half(), torch.zeros(4096, dtype=torch.uint8), torch.ones((1, 64)).half()
+    out = torch.zeros((4, 64)).half()
+    for names in (("out_gate",), ("out_up",), ("out_gate", "out_up")):
+        with pytest.raises(ValueError, match="save=True"):
+            w.gated_gemm(rows, wt, S, wt, S, 64, 64, **{n: out for n in names})

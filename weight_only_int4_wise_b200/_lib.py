@@ -640,7 +640,9 @@ def gated_gemm(A, wt_gate, S_gate, wt_up, S_up, N: int, G: int, act: int = ACT_S
                out_gate=None, out_up=None, flags: int = 0, stream=None):
     """H [M, N] fp16 = act(A x W_gate) * (A x W_up) from activations A [M, K] fp16 and two tiled weight
     matrices [K, N] with scales [ceil(K/G), N]; one rounding. With save=True returns (H, gate, up), the two
-    projections in fp16 as gated_gemm_backward reads them."""
+    projections in fp16 as gated_gemm_backward reads them (out_gate and out_up are where those go)."""
+    if not save and (out_gate is not None or out_up is not None):
+        raise ValueError("out_gate and out_up are written with save=True only")
     return _launch(_gated_gemm, "A", A, stream, wt_gate, S_gate, wt_up, S_up, N, G, act, save, out, out_gate, out_up,
                    flags)
 
