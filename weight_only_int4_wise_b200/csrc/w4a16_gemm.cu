@@ -927,21 +927,24 @@ const Variant& variant_for(int bn) {
 }
 
 struct DeviceState {
-    bool ready = false;
+    bool ready[kKinds] = {};
     int ctas_per_sm[kKinds][kNumVariants] = {};
 };
 
-int prepare_device(DeviceState** out) {
+// Prepares the kernels of one kind on the current device, at its first use: a kind that a
+// process never calls costs it no preparation and no device memory, and cannot refuse
+// another (a first plain product that prepared all four took 32 ms and 8 MB of device
+// memory for code; with its own kind alone 26 ms and 2 MB).
+int prepare_device(Kind kind, DeviceState** out) {
     static DeviceState states[64];
     static std::mutex mu;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W4A16_ERR_CUDA;
     std::lock_guard<std::mutex> lock(mu);
     DeviceState& st = states[dev];
-    if (!st.ready) {
-        for (int i = 0; i < kKinds * kNumVariants; ++i) {
-            const Variant& v = kVariants[i % kNumVariants];
-            const int kind = i / kNumVariants;
+    if (!st.ready[kind]) {
+        for (int i = 0; i < kNumVariants; ++i) {
+            const Variant& v = kVariants[i];
             int n = 1 << 30;
             for (int f = 2 * kind; f < 2 * kind + 2; ++f) {
                 const void* fn = v.fn[f];
@@ -966,9 +969,9 @@ int prepare_device(DeviceState** out) {
                 n = std::min(n, 512 / v.tmem_cols);  // every resident CTA holds its TMEM columns
             }
             if (n < 1) return W4A16_ERR_UNSUPPORTED;
-            st.ctas_per_sm[kind][i % kNumVariants] = n;
+            st.ctas_per_sm[kind][i] = n;
         }
-        st.ready = true;
+        st.ready[kind] = true;
     }
     *out = &st;
     return W4A16_OK;
@@ -1009,7 +1012,7 @@ int plan_dense(int64_t M, int64_t N, int64_t K, Plan* plan, bool need_device, in
     int per_sm = kVariants[vi].nominal_per_sm, sms = 148;
     if (need_device) {
         DeviceState* st = nullptr;
-        int rc = prepare_device(&st);
+        int rc = prepare_device(kind, &st);
         if (rc) return rc;
         per_sm = st->ctas_per_sm[kind][vi];
         sms = sm_count();
@@ -1047,7 +1050,7 @@ int plan_grouped(int64_t E, int64_t total_rows, int64_t N, int64_t K, Plan* plan
     int per_sm = kVariants[vi].nominal_per_sm;
     if (need_device) {
         DeviceState* st = nullptr;
-        int rc = prepare_device(&st);
+        int rc = prepare_device(kInt4, &st);
         if (rc) return rc;
         per_sm = st->ctas_per_sm[kInt4][vi];
     }
