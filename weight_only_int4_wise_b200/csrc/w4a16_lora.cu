@@ -7,10 +7,9 @@
 // LA[i, r, k], summed in fp32 and rounded to fp16, the MMA's operand type (2^-12
 // of the adapter's part, as every weight of it already carries); the second is the
 // shared product with V LB^T added to its fp32 sums before their one rounding
-// (w4a16_decode.cu for M <= 16, w4a16_gemm.cu above). Keeping V apart costs M * R *
-// 2 bytes and a
-// launch, and spares every column tile of the product the R * K products of its
-// rows. The second launch starts as soon as this one's CTAs run: this kernel
+// (w4a16_decode.cu for M <= 16, w4a16_gemm_kernel.cuh above). Keeping V apart costs
+// M * R * 2 bytes and a launch, and spares every column tile of the product the
+// R * K products of its rows. The second launch starts as soon as this one's CTAs run: this kernel
 // signals its dependents only after its own wait for the previous kernel, so
 // whatever this call's caller wrote is complete by then, and the product waits
 // for this kernel only where it reads V.
