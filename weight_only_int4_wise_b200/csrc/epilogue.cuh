@@ -33,13 +33,17 @@ __device__ __forceinline__ __half epilogue_value(float acc, int act) {
 
 // The gate's activation and its derivative, in fp32 on the unrounded
 // projection (the gated product is rounded once, after the multiplication).
-// As above, no form subtracts numbers near one: the normal CDF is erfc(-x / sqrt 2) / 2 and
+// As above, no value subtracts numbers near one: the normal CDF is erfc(-x / sqrt 2) / 2 and
 // both the tanh GELU and SiLU are x * t with t = 1 / (1 + e^(-z)), z = 2 sqrt(2/pi) (x + 0.044715 x^3)
-// or z = x, whose derivative is t + x t (1 - t) z'.
-// The logistic t uses the hardware exponential and division: where the result is
-// not below fp16's range (|z| < 30) their relative error is below 2^-18, against
-// the 2^-11 of its one rounding to fp16, and they take 6 instead of about 25
-// instructions (the gated epilogue at 2048 x 14336: 482 -> 461 us).
+// or z = x, whose derivative is t + x t (1 - t) z'. (The derivative does subtract: from z = 17
+// on 1 + e^(-z) and t are 1 and its second term 0, as the tests with the largest gates see;
+// below, 1 - t is off by a few 2^-24, which x z' carries over: below 2^-16 of a derivative near
+// one, against the 2^-11 of its rounding to fp16.)
+// The logistic t uses the hardware exponential and division. By their published bounds (2 +
+// floor(1.173 |z|) ulp and 2 ulp) the relative error of t is below 2^-17.6 where the result is
+// not below fp16's range (|z| < 30), and below 2^-16.5 with the rounding of the tanh GELU's z,
+// against the 2^-11 of its one rounding to fp16; they take 6 instead of about 25 instructions
+// (the gated epilogue at 2048 x 14336 when it was changed: 482 -> 461 us).
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)

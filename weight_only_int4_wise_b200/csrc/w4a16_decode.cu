@@ -19,10 +19,14 @@
 //     copies by the threads took 7): the operand columns past M read row M - 1, and
 //     their results are dropped;
 //   - the KS partial tiles are added in order through shared memory.
-// Measured (gated, 4096 -> 14336, 60.6 MB): 21.6 us at M = 1..8 (2.8 TB/s), 29.7 at M =
-// 9..16. Between K = 4096 and 8192 a block of 2048 weights takes a sub-partition 308
-// cycles with one token tile and 510 with two: about 22 per MMA, during which its
-// warps issue nothing else, and 130 for the decoding. The MMAs bound it, not HBM.
+// Measured (gated, 4096 -> 14336, 60.6 MB): 21.6 us at M = 1..8 (2.8 TB/s), 30.2 at M =
+// 9..16. No unit is full: DRAM 22-29 %, issue slots 47-52 %, tensor pipe 13-20 %. The
+// largest stall is the wait for global loads (4.7-5.2 cycles per issue): what a warp has
+// in flight lives in its registers, kAhead blocks of about ten. Between K = 4096 and 8192
+// a block of 2048 weights takes a sub-partition 308 cycles with one token tile and 510
+// with two; the difference is eight more MMAs, four more shared loads, and the spills of
+// the two-tile forms (24 to 44 bytes stored at 72 registers; the one-tile forms have
+// none). 1792 warp tiles in CTAs of 13 leave 10 of 148 SMs without work.
 // A chunk of 32 k is four words of 8 codes; inside an MMA the order of k is free as
 // long as both operands use it, so thread t of a quad takes k = 32t + 8v .. + 7 of
 // a block for step w, with v = w for t = 0, 1 and v = w ^ 1 for t = 2, 3: with rows

@@ -42,7 +42,9 @@
 // of one column, a row of a K-major operand tile, and in the epilogue a TMEM lane
 // holds both projections of its column. Against one 128-lane MMA tile of 64 gate and
 // 64 up columns from TMEM (w4a16_gemm_kernel.cuh), which brings the activations in twice as
-// often, 2048 x 4096 -> 14336 takes 417 instead of 461 us (with SiLU).
+// often, 2048 x 4096 -> 14336 takes 417 instead of 470 us (with SiLU). Each row tile
+// reads both weight matrices again (332 MB from DRAM there, for inputs of 77 MB): at 15 %
+// of DRAM's rate that does not bound it.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -696,10 +698,11 @@ int dgrad(int sources, const w4a16_half* const* dC, const uint8_t* const* Wt, co
 // columns per CTA (half the work per CTA and stage, twice the CTAs, and a K split for
 // one row tile). Cycles of a launch on either side, fitted to measured launches: a
 // CTA's start and epilogue, then its stages (decoding bounds a stage here from below
-// at 820), and the exchange of a K split. Measured, this form against the other:
-// 2048 x 4096 -> 14336 417 / 461 us; 700 x 800 -> 9000 26.9 / 39.6; 333 x 1112 -> 2856
-// (G = 48) 15.7 / 18.2; 96 x 4096 -> 14336 38.3 / 41.1; 150 x 4096 -> 4096 36.4 / 20.0;
-// 500 x 2048 -> 4096 21.7 / 19.4.
+// at 820), and the exchange of a K split. Measured, this form against the other (calls
+// through the Python helper): 2048 x 4096 -> 14336 417 / 470 us, 449 / 499 with the
+// projections kept; 700 x 800 -> 9000 27.3 / 39.6; 333 x 1112 -> 2856 (G = 48) 18.5 / 21.6;
+// 96 x 4096 -> 14336 39.5 / 41.6; 150 x 4096 -> 4096 36.5 / 19.4; 500 x 2048 -> 4096
+// 22.4 / 20.3.
 bool wide_gated_takes(int64_t M, int64_t N, int64_t K, int64_t G, int64_t row_tile, int64_t splits,
                       int64_t ctas_per_sm) {
     const int64_t sms = sm_count() > 0 ? sm_count() : 148;

@@ -98,17 +98,17 @@ struct Params {
 // 0..63 hold their gate columns and lanes 64..127 the same up columns, so one
 // MMA sequence over one activation stream makes both projections, at the cost
 // of a dense product twice as wide; the epilogue pairs the two halves. (Few rows,
-// or a K split; w4a16_dgrad.cu takes the gated product of many rows.) Measured: 40 us
-// for 17..64 x 4096 -> 14336, bound by the stages' hand-off and decoding.
+// or a K split; w4a16_dgrad.cu takes the gated product of many rows.) Measured: 38 us
+// for 17 and 32 rows x 4096 -> 14336, 40 for 64, bound by the stages' hand-off and decoding.
 // kLora: the dense product plus V[m] LB[ids[m]]^T. The distinct adapters of the
 // CTA's token tile form further contraction stages behind those of K, 64 values
 // of (adapter, rank) each: the dequantising warps put LB's rows in the weights'
 // TMEM slot and, in the activations' slot, V's rows rounded to fp16 where the row
 // uses that adapter and zeros elsewhere. So the adapters join the same fp32
 // accumulator and cost D * R / 64 more stages for D adapters in the tile. Measured
-// at 2048 x 4096 -> 4096 with rank 16: 64 us without an adapter (the dense product
-// takes 62), 68 with four prompts of one adapter each and one without, 74 when
-// every row has one; V's kernel is part of each.
+// at 2048 x 4096 -> 4096 with rank 16, call after call: 57 us without an adapter (the
+// dense product takes 55), 65 with four prompts of one adapter each and one without, 76
+// with one adapter for all rows, 111 with eight mixed; V's kernel is part of each.
 enum GemmForm { kPlain = 0, kGated = 1, kLora = 2 };
 
 // One kernel of a form and its launch, for one token tile and one kind of group size.

@@ -4,7 +4,7 @@
 // (The Int4GroupwiseGemmPluginV2 page describes the shared projection only.)
 //
 // Two launches. The first, here, makes V[m, r] = scaling[i] * sum_k A[m, k]
-// LA[i, r, k], summed in fp32 and rounded to fp16, the MMA's operand type (2^-12
+// LA[i, r, k], summed in fp32 and rounded to fp16, the MMA's operand type (up to 2^-11
 // of the adapter's part, as every weight of it already carries); the second is the
 // shared product with V LB^T added to its fp32 sums before their one rounding
 // (w4a16_decode.cu for M <= 16, w4a16_gemm_kernel.cuh above). Keeping V apart costs
@@ -20,10 +20,10 @@
 // fragments (16 bytes per lane: inside a block the order of k is free as long
 // as both operands use it), and add their fp32 partials in warp order through
 // shared memory. It is
-// bound by latency (two to eight rounds of loads per warp): 11 us cold at 16 tokens
-// with 16 adapters of rank 64, 28 us in the narrow form at 2048 rows, of which about
-// 10 are not hidden behind the product's K loop. Extra CTAs behind the row groups list the distinct adapters of
-// each token tile of the tensor-core product.
+// bound by latency (two to eight rounds of loads per warp): 8.9 us cold at 16 tokens
+// with 16 adapters of rank 64, 18.7 us in the narrow form at 2048 rows, where the two
+// launches together take 8 us more than without an adapter. Extra CTAs behind the row
+// groups list the distinct adapters of each token tile of the tensor-core product.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -120,11 +120,15 @@ __device__ void list_adapters(const DownParams& p, int z, int* lists /* [8][32] 
     }
 }
 
-// W = 16 warps where this kernel's latency counts. With many row groups W = 4: a CTA
-// of 128 threads and 8 K registers fits on an SM beside the product's CTA (576
-// threads, 55 K registers), so the product's K loop, which needs no V, runs at the
-// same time. (Both ask for the largest shared-memory carve-out: an SM changes it
-// only when it is empty.)
+// W = 16 warps where this kernel's latency counts. With many row groups W = 4: small
+// CTAs leave an SM soon, and the product's CTA (576 threads, 55 K registers) starts
+// there while others still run; at 110 registers a thread it does not start beside one
+// of them (bounded to 80 registers it would: 125 instead of 105 us with 8 adapters mixed
+// over 2048 rows, 95 -> 108 us for a call alone, no gain for prompts). Narrow against wide
+// form, 4096 -> 4096, rank 16: 1024 rows in prompts 36.2 / 38.3 us, 2048 75.1 / 74.6, with
+// rank 64 84.5 / 83.0, one adapter for all 77.5 / 76.1, 8 mixed 105 / 101; 1100 rows ->
+// 14336 138 / 139. (Both kernels ask for the largest shared-memory carve-out: an SM
+// changes it only when it is empty.)
 template <int RT, int W>
 __global__ void __launch_bounds__(W * 32) lora_down_kernel(const DownParams p) {
     constexpr int kWarps = W, kThreads = W * 32;
@@ -222,8 +226,8 @@ __global__ void __launch_bounds__(W * 32) lora_down_kernel(const DownParams p) {
     }
 }
 
-// Row groups from which the product's K loop hides the slower, narrow form.
-constexpr int kOverlapGroups = 64;
+// Row groups from which the narrow form is taken (both sides measured above).
+constexpr int kNarrowGroups = 64;
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -259,7 +263,7 @@ int lora_down(DownParams& p, int tiles, cudaStream_t stream) {
     // Ranks per CTA: few row groups spread the ranks over CTAs (8 each); many
     // keep 16 or 32 together, so that A is read once per 16 or 32 ranks.
     // (The narrow form has registers for 16.)
-    const bool narrow = p.groups >= kOverlapGroups;
+    const bool narrow = p.groups >= kNarrowGroups;
     const int rt = p.groups <= 8 ? 1 : (p.R <= 16 || narrow ? 2 : 4);
     const int chunks = (p.R + 8 * rt - 1) / (8 * rt);
     // Adapters of a group side by side while that leaves one CTA per SM, and always
