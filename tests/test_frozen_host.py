@@ -80,6 +80,8 @@ def test_threads_that_make_first_calls_at_once_do_not_race(tmp_path):
             return wrong.load() || tries[0] != 2 || tries[1] != 2;
         }
     """, flags=("-fsanitize=thread",))
+    if "unexpected memory mapping" in run.stderr:
+        pytest.skip("the race detector does not start under this kernel's address layout")
     assert run.returncode == 0, run.stdout + run.stderr
 
 

@@ -46,8 +46,9 @@ def test_the_plain_product_does_not_prepare_the_other_forms():
     for name in ("plain", "gated"):
         first, later = times[name]
         assert first > 20 * later, (name, times)
-    # ... and neither does loading the code of those forms: their module is as large as the plain products'
-    assert times["gated"][0] > times["plain"][0] / 4, times
+    # ... and neither does loading the code of those forms: it takes about 16 ms, and the preparation alone less than 1
+    # (not measured against the first plain product, which on a cold machine also waits for the file)
+    assert times["gated"][0] > 3e-3, times
 
 
 CAPTURED = """
